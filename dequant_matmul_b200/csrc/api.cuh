@@ -3,6 +3,7 @@
 // Every argument is validated on the host; nothing is launched on an error.
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "hlwq_common.cuh"
@@ -228,6 +229,93 @@ extern "C" int hlwq_kv_window_append(const uint16_t* x, int64_t t, int64_t ldx, 
                                        as_stream(stream));
 }
 
+namespace {
+
+constexpr int64_t kKvMaxTokens = int64_t(1) << 30;
+
+// Sizes shared by the calls of the paged KV cache.
+int kv_page_check(int64_t B, int64_t T, int64_t R, int64_t page_size) {
+  if (B <= 0 || T <= 0 || T > kKvMaxTokens || R < 0 || R > kMaxIn || page_size <= 0) return HLWQ_EINVAL;
+  if (page_size % 16 || page_size > 4096 || B > hlwq::kKvMaxRequests) return HLWQ_EUNSUPPORTED;
+  return HLWQ_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int kv_pool_check(const uint8_t* kp, const uint16_t* kn, const uint8_t* vp, const uint16_t* vn, int64_t num_pages,
+                  const uint16_t* kw, const uint16_t* vw, int64_t R) {
+  if (!kp || !kn || !vp || !vn || num_pages <= 0 || num_pages > INT32_MAX) return HLWQ_EINVAL;
+  if (R > 0 && (!kw || !vw)) return HLWQ_EINVAL;
+  if (!aligned16(kp) || !aligned16(kn) || !aligned16(vp) || !aligned16(vn) || !aligned16(kw) || !aligned16(vw))
+    return HLWQ_EALIGN;
+  return HLWQ_OK;
+}
+
+}  // namespace
+
+extern "C" int hlwq_kv_block_tables(const int32_t* n_past, const int32_t* n_new, int64_t B, int64_t R,
+                                    int64_t page_size, const int32_t* free_pages, int64_t free_cap,
+                                    const int32_t* n_free, int32_t* n_free_out, int32_t* block_table,
+                                    int64_t max_pages, int32_t* cu_new, int64_t* slot_map, int64_t T, void* stream) {
+  if (!n_past || !n_new || !free_pages || !n_free || !n_free_out || !block_table || !cu_new || !slot_map ||
+      n_free == n_free_out || free_cap <= 0 || free_cap > INT32_MAX || max_pages <= 0 || max_pages > INT32_MAX)
+    return HLWQ_EINVAL;
+  if (const int st = kv_page_check(B, T, R, page_size)) return st;
+  if (!aligned4(n_past) || !aligned4(n_new) || !aligned4(free_pages) || !aligned4(n_free) || !aligned4(n_free_out) ||
+      !aligned4(block_table) || !aligned4(cu_new) || (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+    return HLWQ_EALIGN;
+  return hlwq::launch_kv_tables(n_past, n_new, static_cast<int>(B), R, page_size, free_pages, free_cap, n_free,
+                                n_free_out, block_table, max_pages, cu_new, slot_map, T, as_stream(stream));
+}
+
+extern "C" int hlwq_kv_paged_append(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, int64_t T,
+                                    int64_t kv_heads, const int64_t* slot_map, const int32_t* cu_new,
+                                    const int32_t* n_past, int64_t B, const float* codebook8, uint8_t* k_packed,
+                                    uint16_t* k_norms, uint8_t* v_packed, uint16_t* v_norms, int64_t num_pages,
+                                    int64_t page_size, uint16_t* k_window, uint16_t* v_window, int64_t R,
+                                    void* stream) {
+  if (!K || !V || !slot_map || !cu_new || !n_past || !codebook8 || kv_heads <= 0 || ldk < kv_heads * 256 ||
+      ldv < kv_heads * 256)
+    return HLWQ_EINVAL;
+  if (const int st = kv_page_check(B, T, R, page_size)) return st;
+  if (kv_heads > 1024) return HLWQ_EUNSUPPORTED;
+  if (const int st = kv_pool_check(k_packed, k_norms, v_packed, v_norms, num_pages, k_window, v_window, R)) return st;
+  if (!aligned16(K) || !aligned16(V) || ldk % 8 || ldv % 8 || !aligned4(cu_new) || !aligned4(n_past) ||
+      !aligned4(codebook8) || (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+    return HLWQ_EALIGN;
+  return hlwq::launch_kv_append(K, ldk, V, ldv, T, static_cast<int>(kv_heads), slot_map, cu_new, n_past,
+                                static_cast<int>(B), codebook8, k_packed, k_norms, v_packed, v_norms, num_pages,
+                                page_size, k_window, v_window, R, as_stream(stream));
+}
+
+extern "C" int hlwq_kv_paged_attention(const uint16_t* Q, int64_t ldq, int64_t T, int64_t q_heads, int64_t kv_heads,
+                                       float scale, const int32_t* cu_new, const int32_t* n_past, int64_t B,
+                                       int64_t max_new, const int32_t* block_table, int64_t max_pages,
+                                       const float* codebook8, const uint8_t* k_packed, const uint16_t* k_norms,
+                                       const uint8_t* v_packed, const uint16_t* v_norms, int64_t num_pages,
+                                       int64_t page_size, const uint16_t* k_window, const uint16_t* v_window,
+                                       int64_t R, uint16_t* out, int64_t ldo, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  if (!Q || !cu_new || !n_past || !block_table || !codebook8 || !out || kv_heads <= 0 || q_heads <= 0 ||
+      q_heads % kv_heads || ldq < q_heads * 256 || ldo < q_heads * 256 || max_new <= 0 || max_pages <= 0 ||
+      max_pages > INT32_MAX || !std::isfinite(scale))
+    return HLWQ_EINVAL;
+  if (const int st = kv_page_check(B, T, R, page_size)) return st;
+  if (kv_heads > 1024 || q_heads / kv_heads > 64) return HLWQ_EUNSUPPORTED;
+  if (const int st = kv_pool_check(k_packed, k_norms, v_packed, v_norms, num_pages, k_window, v_window, R)) return st;
+  if (!aligned16(Q) || !aligned16(out) || ldq % 8 || ldo % 8 || !aligned4(cu_new) || !aligned4(n_past) ||
+      !aligned4(block_table) || !aligned4(codebook8))
+    return HLWQ_EALIGN;
+  max_new = std::min(max_new, T);
+  const size_t need = hlwq_workspace_bytes(HLWQ_OP_KV_ATTENTION, T, max_new, B, q_heads, kv_heads);
+  if (need && (!workspace || ws_bytes < need)) return HLWQ_EWORKSPACE;
+  if (need && !aligned16(workspace)) return HLWQ_EALIGN;
+  const hlwq::KvAttn a{Q, out, ldq, ldo, T, cu_new, n_past, static_cast<int>(B), static_cast<int>(q_heads),
+                       static_cast<int>(kv_heads), static_cast<int>(q_heads / kv_heads), scale, codebook8, k_packed,
+                       k_norms, v_packed, v_norms, num_pages, page_size, block_table, max_pages, k_window, v_window, R};
+  return hlwq::launch_kv_attention(a, max_new, workspace, ws_bytes, as_stream(stream));
+}
+
 extern "C" int hlwq_gemv(const uint8_t* packed, const uint16_t* norms, const float* codebook, int64_t out,
                          int64_t in, const uint16_t* x, void* y, int ydtype, void* stream) {
   if (!packed || !norms || !codebook || !x || !y || out <= 0 || in <= 0 || in > kMaxIn) return HLWQ_EINVAL;
@@ -347,6 +435,12 @@ extern "C" size_t hlwq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c, 
   if (op == HLWQ_OP_MOE) {
     if (E <= 0 || topk <= 0) return 0;
     return hlwq::moe_workspace_bytes(E, a, b, c, topk);
+  }
+  if (op == HLWQ_OP_KV_ATTENTION) {
+    if (E <= 0 || topk <= 0 || E % topk || E / topk > 64 || topk > 1024 || a > kKvMaxTokens ||
+        c > hlwq::kKvMaxRequests)
+      return 0;
+    return hlwq::kv_attention_workspace_bytes(a, std::min(a, b), c, E, topk);
   }
   return 0;
 }

@@ -20,10 +20,11 @@ HLWQ_OK, HLWQ_EINVAL, HLWQ_EALIGN, HLWQ_EUNSUPPORTED, HLWQ_ECUDA, HLWQ_EWORKSPAC
 HLWQ_ESCRATCH = -6
 NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024 + 64 * 1024
 HLWQ_F32, HLWQ_BF16, HLWQ_F16 = 0, 1, 2
-HLWQ_OP_GEMM, HLWQ_OP_MOE, HLWQ_OP_TQ3_GEMM = 1, 2, 3
+HLWQ_OP_GEMM, HLWQ_OP_MOE, HLWQ_OP_TQ3_GEMM, HLWQ_OP_KV_ATTENTION = 1, 2, 3, 4
 HLWQ_FLAG_WEIGHTS_STATIC = 1
 HLWQ_FLAG_MOE_GROUPED = 2
 DEVERR_CODEBOOK, DEVERR_TIMEOUT, DEVERR_CODE_RANGE = 0x1, 0x2, 0x4
+DEVERR_KV_RANGE, DEVERR_KV_PAGES = 0x8, 0x10
 BLOCK, BLOCK_BYTES, LEVELS = 128, 80, 32
 
 # (name, restype, argtypes) for every symbol include/hlwq.h declares.
@@ -44,6 +45,11 @@ SIGNATURES = {
     "hlwq_kv_scores": (_I, [_P, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _P]),
     "hlwq_kv_window_append": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
     "hlwq_kv_scores_window": (_I, [_P, _I64, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _P, _I64, _P]),
+    "hlwq_kv_block_tables": (_I, [_P, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P]),
+    "hlwq_kv_paged_append": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _P,
+                                  _I64, _P]),
+    "hlwq_kv_paged_attention": (_I, [_P, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _P, _I64, _I64, _P, _I64, _P, _P, _P,
+                                     _P, _P, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "hlwq_gemv": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I, _P]),
     "hlwq_gemv_ex": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I, ctypes.c_uint, _P]),
     "hlwq_gemm": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _I64, _I, _P, _SZ, _P]),
@@ -360,6 +366,237 @@ class KVWindowCache:
                                          self.n_enc, _ptr(self.window), self.R, self.n_total, _ptr(S), S.stride(0),
                                          _stream(stream)), "hlwq_kv_scores_window")
         return S
+
+
+class _on:
+    """Makes a tensor's device the current one for a launch (a no-op when it
+    already is), so that the call and torch's current stream belong to it."""
+
+    def __init__(self, t: torch.Tensor, what: str, *others):
+        for o in others:
+            if o is not None and o.device != t.device:
+                raise HLWQError(f"{what}: tensors on {t.device} and {o.device}")
+        here = torch.cuda.current_device()
+        self.guard = None if t.device.index == here else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _array(t: torch.Tensor, name: str, dtype, shape):
+    """A contiguous CUDA tensor of this type and shape (None: any size)."""
+    _cuda(t, name)
+    if t.dtype != dtype:
+        raise HLWQError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise HLWQError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _heads(t: torch.Tensor, name: str):
+    """A bf16 CUDA tensor [T][heads][256] whose tokens are contiguous (any pitch
+    from token to token)."""
+    if not t.is_cuda:
+        raise HLWQError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise HLWQError(f"{name} must be bfloat16, not {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != 256 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 256):
+        raise HLWQError(f"{name} must be [T][heads][256] with contiguous tokens")
+
+
+def _pitch(t: torch.Tensor) -> int:
+    """Elements from token to token (a single token's own length: its stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * 256
+
+
+def _pool(k_pages, v_pages, window, B: int):
+    """Checks the pages and windows of a paged cache; (num_pages, kv_heads, page_size, R)."""
+    packed = k_pages[0]
+    if packed.dim() != 4:
+        raise HLWQError("packed pages must be [num_pages][kv_heads][page_size][96]")
+    n, h, p, _ = packed.shape
+    for name, (pk, nr) in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _array(pk, f"{name} packed", torch.uint8, (n, h, p, 96))
+        _array(nr, f"{name} norms", torch.uint16, (n, h, p))
+    R = 0
+    if window is not None:
+        if window[0].dim() != 4:
+            raise HLWQError("windows must be [B][kv_heads][R][256]")
+        R = window[0].shape[2]
+        for name, w in (("k window", window[0]), ("v window", window[1])):
+            _array(w, name, torch.bfloat16, (B, h, R, 256))
+    return n, h, p, R
+
+
+def kv_block_tables(n_past, n_new, free_pages, n_free, block_table, page_size: int, R: int, T: int = None,
+                    n_free_out=None, cu_new=None, slot_map=None, stream=None):
+    """Block tables and slot maps of one step, from the requests' lengths (all
+    int32 on the device): n_past, n_new [B], the stack free_pages with
+    n_free [1] free entries, block_table [B][max_pages] (updated in place).
+    T is the number of rows of the step's K, V and Q (given by slot_map, if
+    that is passed).  Returns (cu_new int32 [B + 1], slot_map int64 [T],
+    n_free_out int32 [1])."""
+    _array(n_past, "n_past", torch.int32, (None,))
+    B = n_past.shape[0]
+    _array(n_new, "n_new", torch.int32, (B,))
+    _array(free_pages, "free_pages", torch.int32, (None,))
+    _array(n_free, "n_free", torch.int32, (1,))
+    _array(block_table, "block_table", torch.int32, (B, None))
+    if slot_map is None:
+        if T is None:
+            raise HLWQError("kv_block_tables needs T or slot_map")
+        slot_map = torch.empty(T, dtype=torch.int64, device=n_past.device)
+    if n_free_out is None:
+        n_free_out = torch.empty(1, dtype=torch.int32, device=n_past.device)
+    if cu_new is None:
+        cu_new = torch.empty(B + 1, dtype=torch.int32, device=n_past.device)
+    _array(slot_map, "slot_map", torch.int64, (T,))
+    _array(n_free_out, "n_free_out", torch.int32, (1,))
+    _array(cu_new, "cu_new", torch.int32, (B + 1,))
+    with _on(n_past, "kv_block_tables", n_new, free_pages, n_free, n_free_out, block_table, cu_new, slot_map):
+        _check(lib.hlwq_kv_block_tables(_ptr(n_past), _ptr(n_new), B, R, page_size, _ptr(free_pages),
+                                        free_pages.shape[0], _ptr(n_free), _ptr(n_free_out), _ptr(block_table),
+                                        block_table.shape[1], _ptr(cu_new), _ptr(slot_map), slot_map.shape[0],
+                                        _stream(stream)), "hlwq_kv_block_tables")
+    return cu_new, slot_map, n_free_out
+
+
+def kv_paged_append(K, V, slot_map, cu_new, n_past, k_pages, v_pages, window, cb8, stream=None):
+    """K, V bf16 [T][kv_heads][256]: encodes what leaves the window into the
+    pages and keeps the rest exact, both in place.  k_pages, v_pages =
+    (packed uint8 [num_pages][kv_heads][P][96], norms uint16 [num_pages][kv_heads][P]);
+    window = (k, v) bf16 [B][kv_heads][R][256], or None (R = 0: every token is
+    encoded); slot_map and cu_new as kv_block_tables gives them, n_past the
+    lengths before the step."""
+    _heads(K, "K")
+    _heads(V, "V")
+    T, H = K.shape[0], K.shape[1]
+    _array(n_past, "n_past", torch.int32, (None,))
+    B = n_past.shape[0]
+    _array(cu_new, "cu_new", torch.int32, (B + 1,))
+    _array(slot_map, "slot_map", torch.int64, (T,))
+    _array(cb8, "cb8", torch.float32, (8,))
+    n, h, P, R = _pool(k_pages, v_pages, window, B)
+    if V.shape != K.shape or h != H:
+        raise HLWQError(f"K {list(K.shape)}, V {list(V.shape)} and pages of {h} heads do not go together")
+    kw, vw = window if window is not None else (None, None)
+    with _on(K, "kv_paged_append", V, slot_map, cu_new, n_past, *k_pages, *v_pages, kw, vw, cb8):
+        _check(lib.hlwq_kv_paged_append(_ptr(K), _pitch(K), _ptr(V), _pitch(V), T, H, _ptr(slot_map), _ptr(cu_new),
+                                        _ptr(n_past), B, _ptr(cb8), _ptr(k_pages[0]), _ptr(k_pages[1]),
+                                        _ptr(v_pages[0]), _ptr(v_pages[1]), n, P, _ptr(kw), _ptr(vw), R,
+                                        _stream(stream)), "hlwq_kv_paged_append")
+
+
+def kv_attention_workspace(Q, kv_heads: int, B: int, max_new: int) -> int:
+    """Workspace bytes of kv_paged_attention for Q [T][q_heads][256]."""
+    return workspace_bytes(HLWQ_OP_KV_ATTENTION, Q.shape[0], max_new, B, Q.shape[1], kv_heads)
+
+
+def kv_paged_attention(Q, cu_new, n_past, block_table, k_pages, v_pages, window, cb8, max_new: int, scale=None,
+                       out=None, workspace=None, stream=None):
+    """Q bf16 [T][q_heads][256] -> out bf16 [T][q_heads][256]: causal attention
+    of the step's new tokens over their requests' cached tokens and themselves,
+    after kv_paged_append.  max_new bounds the new tokens of one request;
+    scale defaults to 1 / 16.  Rows behind the last request's stay as they are."""
+    _heads(Q, "Q")
+    T, Hq = Q.shape[0], Q.shape[1]
+    _array(n_past, "n_past", torch.int32, (None,))
+    B = n_past.shape[0]
+    _array(cu_new, "cu_new", torch.int32, (B + 1,))
+    _array(block_table, "block_table", torch.int32, (B, None))
+    _array(cb8, "cb8", torch.float32, (8,))
+    n, H, P, R = _pool(k_pages, v_pages, window, B)
+    if Hq % H:
+        raise HLWQError(f"{Hq} query heads are not a multiple of {H} kv heads")
+    if out is None:
+        out = torch.empty(T, Hq, 256, dtype=torch.bfloat16, device=Q.device)
+    _heads(out, "out")
+    if out.shape != Q.shape:
+        raise HLWQError(f"out must be {list(Q.shape)}, not {list(out.shape)}")
+    kw, vw = window if window is not None else (None, None)
+    with _on(Q, "kv_paged_attention", cu_new, n_past, block_table, *k_pages, *v_pages, kw, vw, cb8, out, workspace):
+        if workspace is None:
+            need = kv_attention_workspace(Q, H, B, max_new)
+            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+        _check(lib.hlwq_kv_paged_attention(_ptr(Q), _pitch(Q), T, Hq, H, 1.0 / 16.0 if scale is None else scale,
+                                           _ptr(cu_new), _ptr(n_past), B, max_new, _ptr(block_table),
+                                           block_table.shape[1], _ptr(cb8), _ptr(k_pages[0]), _ptr(k_pages[1]),
+                                           _ptr(v_pages[0]), _ptr(v_pages[1]), n, P, _ptr(kw), _ptr(vw), R, _ptr(out),
+                                           _pitch(out), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                           _stream(stream)), "hlwq_kv_paged_attention")
+    return out
+
+
+class PagedKVCache:
+    """The paged Q3 KV cache of one layer for a batch of request rows: the pool,
+    tables, windows and lengths of hlwq_kv_block_tables / hlwq_kv_paged_append /
+    hlwq_kv_paged_attention, in device memory.  Bookkeeping only; the device
+    work is the library's.  One step of the batch, all of it on the stream and
+    without a host synchronisation (so it can be captured and replayed):
+
+        cache.begin(n_new, T)        # int32 [B] on the device; rows of K, V, Q
+        cache.append(K, V)
+        out = cache.attention(Q, max_new)
+        cache.end()                  # n_new joins n_past
+    """
+
+    def __init__(self, requests: int, kv_heads: int, num_pages: int, max_pages: int, page_size: int = 64, R: int = 128,
+                 device="cuda", cb8=None):
+        shape = (num_pages, kv_heads, page_size)
+
+        def pages():
+            return (torch.zeros(*shape, 96, dtype=torch.uint8, device=device),
+                    torch.zeros(shape, dtype=torch.uint16, device=device))
+
+        def ints(*size, value=0):
+            return torch.full(size, value, dtype=torch.int32, device=device)
+
+        self.k_pages, self.v_pages = pages(), pages()
+        self.window = None
+        if R:
+            self.window = tuple(torch.zeros(requests, kv_heads, R, 256, dtype=torch.bfloat16, device=device)
+                                for _ in range(2))
+        self.B, self.page_size, self.R = requests, page_size, R
+        self.block_table = ints(requests, max_pages, value=-1)
+        self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=device)
+        self.n_free, self._n_free_next = ints(1, value=num_pages), ints(1, value=num_pages)
+        self.n_past, self.cu_new = ints(requests), ints(requests + 1)
+        self.n_new = self.slot_map = None
+        self.cb8 = cb8 if cb8 is not None else kv_codebook(device)
+
+    def begin(self, n_new: torch.Tensor, T: int, slot_map=None, stream=None):
+        """Pages and slots of a step in which request b gets n_new[b] tokens."""
+        self.n_new = n_new
+        _, self.slot_map, _ = kv_block_tables(self.n_past, n_new, self.free_pages, self.n_free, self.block_table,
+                                              self.page_size, self.R, T, self._n_free_next, self.cu_new, slot_map, stream)
+
+    def append(self, K: torch.Tensor, V: torch.Tensor, stream=None):
+        kv_paged_append(K, V, self.slot_map, self.cu_new, self.n_past, self.k_pages, self.v_pages, self.window, self.cb8,
+                        stream)
+
+    def attention(self, Q: torch.Tensor, max_new: int, scale=None, out=None, workspace=None, stream=None):
+        return kv_paged_attention(Q, self.cu_new, self.n_past, self.block_table, self.k_pages, self.v_pages, self.window,
+                                  self.cb8, max_new, scale, out, workspace, stream)
+
+    def end(self, stream=None):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.n_past.device)):
+            self.n_past += self.n_new
+            self.n_free.copy_(self._n_free_next)
+
+    def release(self, b: int):
+        """Empties request row b and gives its pages back (reads its length: synchronises)."""
+        k = -(-max(0, int(self.n_past[b]) - self.R) // self.page_size)
+        k = min(k, self.block_table.shape[1])
+        n = int(self.n_free)
+        self.free_pages[n:n + k] = self.block_table[b, :k]
+        self.n_free += k
+        self.block_table[b] = -1
+        self.n_past[b] = 0
 
 
 def gemv(packed, norms, cb, x: torch.Tensor, out_dtype=torch.float32, y=None, stream=None, flags: int = 0):

@@ -19,7 +19,8 @@
  * Dequantisation: w_hat[o][128b + i] = n16[o][b] / 128 * sum_j c[k_obj] H[j][i].
  *
  * Also declared here: the Q5 -> INT4 re-encoder, the Q3 KV-cache encoding
- * with its residual window, the TQ3 (scalar HIGGS) weight format with its
+ * with its residual window, the paged batch form of that cache (block tables,
+ * append, attention), the TQ3 (scalar HIGGS) weight format with its
  * fused GEMV and small-M GEMM, and the conversion between the packed codes
  * and one code per byte.
  *
@@ -68,7 +69,7 @@ typedef enum {
 typedef enum { HLWQ_F32 = 0, HLWQ_BF16 = 1, HLWQ_F16 = 2 } hlwq_dtype;
 
 /* Operations whose scratch size hlwq_workspace_bytes() reports. */
-typedef enum { HLWQ_OP_GEMM = 1, HLWQ_OP_MOE = 2, HLWQ_OP_TQ3_GEMM = 3 } hlwq_op;
+typedef enum { HLWQ_OP_GEMM = 1, HLWQ_OP_MOE = 2, HLWQ_OP_TQ3_GEMM = 3, HLWQ_OP_KV_ATTENTION = 4 } hlwq_op;
 
 /* Launch flags of the *_ex calls. */
 typedef enum { HLWQ_FLAG_WEIGHTS_STATIC = 1, HLWQ_FLAG_MOE_GROUPED = 2 } hlwq_flags;
@@ -77,6 +78,8 @@ typedef enum { HLWQ_FLAG_WEIGHTS_STATIC = 1, HLWQ_FLAG_MOE_GROUPED = 2 } hlwq_fl
 #define HLWQ_DEVERR_CODEBOOK 0x1u  /* codebook not strictly ascending or not finite */
 #define HLWQ_DEVERR_TIMEOUT  0x2u  /* a bounded in-kernel wait gave up */
 #define HLWQ_DEVERR_CODE_RANGE 0x4u  /* hlwq_codes_pack met a code above 31 */
+#define HLWQ_DEVERR_KV_RANGE 0x8u    /* a length, offset, slot or page of the paged KV cache is out of range */
+#define HLWQ_DEVERR_KV_PAGES 0x10u   /* hlwq_kv_block_tables: the page pool or a table row is exhausted */
 
 /*
  * Lloyd-Max codebook for N(0,1) (Method step [4]: "Lloyd-Max 5-bit quantization
@@ -202,6 +205,86 @@ int hlwq_kv_scores_window(const uint16_t* q, int64_t m, int64_t ldq, const uint8
                           const uint16_t* norms, const float* codebook8, int64_t n_enc,
                           const uint16_t* window, int64_t R, int64_t n_total, float* scores, int64_t lds,
                           void* stream);
+
+/*
+ * The paged Q3 KV cache: the encoding and residual window of hlwq_kv_* for a
+ * batch of requests and kv_heads heads, with the encoded tokens in pages, so
+ * that requests of any lengths share one pool.  One serving step is
+ * hlwq_kv_block_tables, hlwq_kv_paged_append, hlwq_kv_paged_attention.  All
+ * lengths are device data: a step can be captured in a CUDA graph and replayed
+ * with other lengths.
+ *
+ * Request b (a row 0 .. B - 1) has n_past[b] tokens cached and n_new[b] >= 0
+ * tokens in this step.  Of N = n_past + n_new tokens the last min(N, R) are
+ * exact, token i in ring slot i % R; the max(0, N - R) before them are encoded
+ * as hlwq_kv_quantize does, P = page_size tokens to a page (R = 0: all are
+ * encoded).
+ *   n_past, n_new  int32 [B]
+ *   cu_new         int32 [B + 1]: new tokens before request b, cu_new[B] of all.
+ *                  Token j of request b is row cu_new[b] + j of K, V, Q, out;
+ *                  rows cu_new[B] .. T - 1 are neither read nor written
+ *   block_table    int32 [B][max_pages]: page of tokens [kP, kP + P) at [b][k]
+ *   slot_map       int64 [T]: where the token goes that leaves the window as
+ *                  new token t enters (token n_past + j - R of its request):
+ *                  page * P + offset, or -1 when none leaves
+ *   k_packed, v_packed  uint8 [num_pages][kv_heads][P][96]
+ *   k_norms, v_norms    uint16 [num_pages][kv_heads][P]: binary16 bits
+ *   k_window, v_window  bf16 [B][kv_heads][R][256], or NULL when R = 0
+ *   K, V           bf16 [T][kv_heads][256], Q and out [T][q_heads][256]; a
+ *                  token's heads are contiguous, ldk / ldv / ldq / ldo elements
+ *                  from token to token
+ *
+ * hlwq_kv_block_tables: cu_new, slot_map and the block-table entries of the
+ *   pages that this step needs first.  Pages come from the stack free_pages
+ *   [free_cap], whose entries [0, n_free[0]) are free, last entry first, in
+ *   the order of the requests; n_free_out[0] (another word than n_free, so
+ *   that a repeated call repeats its result) is what stays free.  Table
+ *   entries of pages in use are read only.  A page that is not to be had (the
+ *   pool is empty, or the row of max_pages is full) raises
+ *   HLWQ_DEVERR_KV_PAGES; its entry and slots are -1.  Negative lengths count
+ *   as 0 and, like sum n_new > T, raise HLWQ_DEVERR_KV_RANGE.
+ * hlwq_kv_paged_append: encodes every token that leaves (from its ring slot,
+ *   or from K / V when the chunk is longer than the window) into its slot,
+ *   codes and norms as those of hlwq_kv_quantize, and copies the new tokens
+ *   that stay into the ring; one launch.  n_past is the length before the
+ *   step.  A token whose slot is not a slot of the pool is not stored and
+ *   raises HLWQ_DEVERR_KV_RANGE, as do requests whose rows are not in [0, T).
+ * hlwq_kv_paged_attention: out = softmax(scale * q . k) v for every new token
+ *   over the tokens up to itself, after the append of the same step; query
+ *   heads g kv_heads-major (q_heads = kv_heads * group, head h * group + g
+ *   reads kv head h).  fp32 softmax and sums, binary16 operands in the rotated
+ *   domain, out rounded to bf16 once.  Keys in pages that are not in
+ *   [0, num_pages) are left out (HLWQ_DEVERR_KV_RANGE).  A request may have
+ *   at most max_new tokens in the step; more raise HLWQ_DEVERR_KV_RANGE and
+ *   the rows past the limit may stay unwritten.
+ *   workspace  device, 16-byte aligned, ws_bytes >= hlwq_workspace_bytes(
+ *              HLWQ_OP_KV_ATTENTION, T, max_new, B, q_heads, kv_heads); its
+ *              contents need not survive between calls, and calls that may
+ *              overlap need one each
+ * Errors: HLWQ_EINVAL (NULL, sizes: B, T, max_pages, num_pages, kv_heads,
+ * max_new <= 0; T > 2^30; R < 0 or > 2^20; q_heads not a multiple of kv_heads;
+ * ld below heads * 256; n_free_out == n_free; scale not finite),
+ * HLWQ_EUNSUPPORTED (page_size not a multiple of 16 in 16 .. 4096; B > 8192;
+ * q_heads / kv_heads > 64; kv_heads > 1024), HLWQ_EALIGN (packed, norms,
+ * windows, K, V, Q, out and workspace 16-byte, ld a multiple of 8 elements,
+ * int32 arrays 4-byte, slot_map 8-byte), HLWQ_EWORKSPACE, HLWQ_ECUDA.
+ */
+int hlwq_kv_block_tables(const int32_t* n_past, const int32_t* n_new, int64_t B, int64_t R, int64_t page_size,
+                         const int32_t* free_pages, int64_t free_cap, const int32_t* n_free, int32_t* n_free_out,
+                         int32_t* block_table, int64_t max_pages, int32_t* cu_new, int64_t* slot_map, int64_t T,
+                         void* stream);
+int hlwq_kv_paged_append(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, int64_t T,
+                         int64_t kv_heads, const int64_t* slot_map, const int32_t* cu_new, const int32_t* n_past,
+                         int64_t B, const float* codebook8, uint8_t* k_packed, uint16_t* k_norms,
+                         uint8_t* v_packed, uint16_t* v_norms, int64_t num_pages, int64_t page_size,
+                         uint16_t* k_window, uint16_t* v_window, int64_t R, void* stream);
+int hlwq_kv_paged_attention(const uint16_t* Q, int64_t ldq, int64_t T, int64_t q_heads, int64_t kv_heads,
+                            float scale, const int32_t* cu_new, const int32_t* n_past, int64_t B, int64_t max_new,
+                            const int32_t* block_table, int64_t max_pages, const float* codebook8,
+                            const uint8_t* k_packed, const uint16_t* k_norms, const uint8_t* v_packed,
+                            const uint16_t* v_norms, int64_t num_pages, int64_t page_size,
+                            const uint16_t* k_window, const uint16_t* v_window, int64_t R, uint16_t* out,
+                            int64_t ldo, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * TQ3 weights, the scalar case of HIGGS ("Qwen3.6-35B-A3B-TQ3-native", "What
@@ -355,6 +438,7 @@ int hlwq_moe_gemv_ex(const uint8_t* gu_packed, const uint16_t* gu_norms,
  *   HLWQ_OP_GEMM: a = out, b = in, c = M
  *   HLWQ_OP_MOE : a = H,   b = F,  c = T, E = experts, topk
  *   HLWQ_OP_TQ3_GEMM: a = out, b = in, c = M
+ *   HLWQ_OP_KV_ATTENTION: a = T, b = max_new, c = B, E = q_heads, topk = kv_heads
  */
 size_t hlwq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c, int64_t E, int64_t topk);
 

@@ -1,0 +1,499 @@
+"""GPU tests of the paged Q3 KV cache against the oracle: tables, slots, codes,
+norms and window bit-exact, attention within the oracle's derived tolerance."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from dequant_matmul_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def hl():
+    from dequant_matmul_b200 import hlwq
+    return hlwq
+
+
+@pytest.fixture(scope="module")
+def cb8(hl):
+    return hl.kv_codebook("cuda")
+
+
+def _ints(v, dtype=torch.int32):
+    return torch.tensor(v, dtype=dtype, device="cuda")
+
+
+def _rows(n, H, seed, spikes=True):
+    X = synth.activations(n * H, 256, seed=seed).float().reshape(n, H, 256)
+    if spikes:
+        X[..., :3] *= 30.0   # a few large channels, as keys have
+    return X.to(torch.bfloat16)
+
+
+# ------------------------------------------------------------------ tables
+@pytest.mark.parametrize("B,past,new,P,R,pad", [
+    (1, 0, 1, 16, 0, 0), (1, 127, 2, 16, 128, 1), (3, 500, 1, 64, 128, 0), (33, 300, 1, 48, 31, 7),
+    (5, 700, 900, 16, 1, 3), (1030, 40, 3, 16, 5, 2), (4, 0, 4000, 256, 128, 0)])
+def test_block_tables(hl, B, past, new, P, R, pad):
+    rng = np.random.default_rng(B + past + new)
+    n_past, n_new = rng.integers(0, past + 1, B), rng.integers(0, new + 1, B)
+    n_past[0], n_new[0] = past, new
+    held = [O.kv_pages(int(p), P, R) for p in n_past]
+    need = sum(O.kv_pages(int(p + n), P, R) for p, n in zip(n_past, n_new))
+    order = rng.permutation(need + 9)
+    width = max(1, max(O.kv_pages(int(p + n), P, R) for p, n in zip(n_past, n_new)))
+    table = np.full((B, width), -1)
+    at = 0
+    for b, k in enumerate(held):
+        table[b, :k] = order[at:at + k]
+        at += k
+    free, T = order[at:], int(n_new.sum()) + pad
+    want = O.kv_block_tables(n_past, n_new, free, table, P, R, T)
+    t, out, cu = _ints(table), torch.full((1,), -7, dtype=torch.int32, device="cuda"), None
+    for _ in range(2):   # a repeated call repeats its result
+        cu, slots, left = hl.kv_block_tables(_ints(n_past), _ints(n_new), _ints(free), _ints([len(free)]), t, P, R, T,
+                                             n_free_out=out)
+        torch.cuda.synchronize()
+        assert np.array_equal(t.cpu().numpy(), want[0])
+        assert np.array_equal(cu.cpu().numpy(), want[1])
+        assert np.array_equal(slots.cpu().numpy(), want[2])
+        assert int(left) == want[3]
+    assert hl.device_error() == 0
+
+
+def test_block_tables_without_enough_pages(hl):
+    """The pool gives out its last page and then -1; a full table row likewise."""
+    hl.device_error()
+    past, new, free = [0, 0, 100], [40, 40, 1], [3, 1, 2]
+    table = np.full((3, 7), -1)
+    table[2, :7] = range(10, 17)
+    want = O.kv_block_tables(past, new, free, table, 16, 0, 81)
+    t = _ints(table)
+    cu, slots, left = hl.kv_block_tables(_ints(past), _ints(new), _ints(free), _ints([3]), t, 16, 0, 81)
+    assert hl.device_error() == hl.DEVERR_KV_PAGES
+    assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(slots.cpu().numpy(), want[2])
+    assert (want[2] == -1).sum() == 40 and int(left) == 0
+    t = _ints(table[:, :2])   # rows of two pages: tokens from 32 on have no place
+    cu, slots, left = hl.kv_block_tables(_ints(past), _ints(new), _ints(range(20, 40)), _ints([20]), t, 16, 0, 81)
+    assert hl.device_error() == hl.DEVERR_KV_PAGES
+    want = O.kv_block_tables(past, new, range(20, 40), table[:, :2], 16, 0, 81)
+    assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(slots.cpu().numpy(), want[2])
+    assert int(left) == 16
+
+
+def test_block_tables_with_lengths_out_of_range(hl):
+    hl.device_error()
+    t = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    cu, slots, left = hl.kv_block_tables(_ints([-5, 3]), _ints([2, -1]), _ints([0, 1]), _ints([2]), t, 16, 0, 4)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
+    assert cu.tolist() == [0, 2, 2] and slots.tolist() == [16, 17, -1, -1] and int(left) == 1
+    # more new tokens than rows
+    hl.kv_block_tables(_ints([0, 0]), _ints([3, 3]), _ints([0, 1]), _ints([2]), t, 16, 0, 4)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
+
+
+# ------------------------------------------------------------------ a batch for append and attention
+def _batch(past, new, H, P, R, seed, spikes=True):
+    """Host state of a batch with its pages interleaved in a pool."""
+    rng = np.random.default_rng(seed)
+    B = len(past)
+    need = sum(O.kv_pages(p + n, P, R) for p, n in zip(past, new))
+    order = rng.permutation(need + 3)
+    width = max(1, max(O.kv_pages(p + n, P, R) for p, n in zip(past, new))) + 1
+    table, at = np.full((B, width), -1), 0
+    for b, p in enumerate(past):
+        k = O.kv_pages(p, P, R)
+        table[b, :k] = order[at:at + k]
+        at += k
+    T = sum(new)
+    table, cu, slots, _ = O.kv_block_tables(past, new, order[at:], table, P, R, T)
+    kv = []
+    for which in range(2):
+        X = _rows(T, H, seed + 10 + which, spikes and which == 0)
+        if T > 2:
+            X[1] = 0    # a zero vector
+        win = _rows(B * max(R, 1), H, seed + 20 + which).reshape(B, max(R, 1), H, 256).transpose(1, 2)[:, :, :R]
+        old = O.kv_quantize(_rows(order.size * P, H, seed + 30 + which, spikes and which == 0).reshape(-1, 256))
+        kv.append((X, win.contiguous(), old["packed"].reshape(order.size, P, H, 96).swapaxes(1, 2).copy(),
+                   old["norms"].reshape(order.size, P, H).swapaxes(1, 2).copy()))
+    return table, cu, slots, kv
+
+
+def _dev_pages(packed, norms):
+    return torch.from_numpy(packed.copy()).cuda(), torch.from_numpy(norms.copy().view(np.uint16)).cuda()
+
+
+APPENDS = [([0], [1], 1, 16, 0), ([5], [1], 2, 16, 1), ([130, 0, 127, 64], [1, 1, 1, 1], 3, 64, 128),
+           ([10, 0, 3], [7, 0, 300], 2, 48, 31), ([200, 1], [65, 128], 4, 16, 64), ([100], [17], 5, 256, 0),
+           ([40, 40, 0, 0, 9], [3, 0, 0, 40, 0], 1, 16, 7)]
+
+
+@pytest.mark.parametrize("past,new,H,P,R", APPENDS)
+def test_append(hl, cb8, past, new, H, P, R):
+    table, cu, slots, kv = _batch(past, new, H, P, R, seed=sum(past) + R)
+    T = sum(new)
+    dev, want = [], []
+    for X, win, packed, norms in kv:
+        want.append(O.kv_paged_append(X, slots, cu, past, packed, norms, win.double().numpy(), R))
+        wide = torch.full((T + 2, H * 256 + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:T, :H * 256] = X.reshape(T, -1).cuda()     # rows behind the last request are not read
+        dev.append((wide[:, :H * 256].unflatten(1, (H, 256)), win.cuda() if R else None, _dev_pages(packed, norms)))
+    (K, kw, kp), (V, vw, vp) = dev
+    hl.kv_paged_append(K, V, _ints(list(slots) + [-1, -1], torch.int64), _ints(cu), _ints(past), kp, vp,
+                       (kw, vw) if R else None, cb8)
+    torch.cuda.synchronize()
+    for (_, w, (p, n)), (wp, wn, ww) in zip(dev, want):
+        assert np.array_equal(p.cpu().numpy(), wp)
+        assert np.array_equal(n.cpu().numpy(), wn.view(np.uint16))
+        if R:
+            assert np.array_equal(w.double().cpu().numpy(), ww)
+    assert hl.device_error() == 0
+
+
+def test_append_near_the_borders(hl, cb8):
+    """Vectors whose rotated values lie on, or a few units of fp32 beside, a
+    decision border, and norms next to a binary16 rounding border: the codes and
+    norms are still those of the fp64 definition."""
+    rng = np.random.default_rng(1)
+    n = 4096
+    X = np.zeros((n, 256))
+    # few distinct integers: rotated values are integers and repeat, norms are roots of integers
+    X[:, :] = rng.integers(-2, 3, (n, 256)) * 2.0 ** rng.integers(-60, 60, (n, 1))
+    X[: n // 2, 4:] = 0
+    X[5] = 0
+    X = torch.from_numpy(X).to(torch.bfloat16)
+    want = O.kv_quantize(X)
+    H, P = 4, 64
+    T = n // H
+    pages = [(torch.zeros(T // P, H, P, 96, dtype=torch.uint8, device="cuda"),
+              torch.zeros(T // P, H, P, dtype=torch.uint16, device="cuda")) for _ in range(2)]
+    x = X.reshape(T, H, 256).cuda()
+    hl.kv_paged_append(x, x, torch.arange(T, device="cuda"), _ints([0, T]), _ints([0]), *pages, None, cb8)
+    torch.cuda.synchronize()
+    for p, nr in pages:
+        got = p.transpose(1, 2).reshape(n, 96).cpu().numpy()
+        bad = O.unpack_codes(got, bits=3) != want["codes"]
+        if bad.any():   # two fp64 evaluations may differ only where they cannot tell
+            _, mid, _ = O.codebook_fp32(8)
+            assert np.all(np.min(np.abs(want["y"][bad][:, None] - mid[None, :]), axis=1) < 1e-12)
+        assert np.array_equal(nr.transpose(1, 2).reshape(n).cpu().numpy(), want["norms"].view(np.uint16))
+
+
+def test_append_with_slots_out_of_range(hl, cb8):
+    """A slot that is not one of the pool is not written, and is reported."""
+    hl.device_error()
+    pages = [(torch.zeros(2, 1, 16, 96, dtype=torch.uint8, device="cuda"),
+              torch.zeros(2, 1, 16, dtype=torch.uint16, device="cuda")) for _ in range(2)]
+    x = _rows(3, 1, 5).cuda()
+    hl.kv_paged_append(x, x, _ints([3, 32, -1], torch.int64), _ints([0, 3]), _ints([0]), *pages, None, cb8)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
+    for p, n in pages:
+        assert n.view(torch.int16).reshape(-1).nonzero().tolist() == [[3]]
+    # offsets past the rows, and negative lengths
+    for cu, past in (([0, 9], [0]), ([2, 1], [0]), ([0, 3], [-1])):
+        hl.kv_paged_append(x, x, _ints([4, 5, 6], torch.int64), _ints(cu), _ints(past), *pages, None, cb8)
+        assert hl.device_error() & ~hl.DEVERR_KV_RANGE == 0
+    for p, n in pages:
+        assert n.view(torch.int16).reshape(-1).nonzero().tolist() == [[3]]
+
+
+# ------------------------------------------------------------------ attention
+ATTENTIONS = [
+    # past, new, H, G, P, R
+    ([0], [1], 1, 1, 16, 0), ([0], [1], 2, 6, 64, 128), ([1], [1], 1, 8, 16, 1), ([15], [1], 1, 4, 16, 0),
+    ([16], [1], 1, 4, 16, 0), ([63, 64, 65], [1, 1, 1], 2, 6, 64, 0), ([299], [1], 4, 6, 64, 128),
+    ([128], [1], 2, 6, 64, 128), ([1000, 3, 0, 517], [1, 1, 1, 1], 2, 6, 64, 128), ([700, 60], [1, 0], 1, 16, 48, 31),
+    ([513], [1], 3, 3, 256, 64), ([400, 33], [1, 1], 1, 64, 16, 7), ([250], [1], 2, 17, 16, 128),
+    # a few tokens each
+    ([100, 0, 255], [3, 4, 2], 2, 4, 16, 0), ([300, 77], [2, 2], 1, 8, 64, 128), ([90], [5], 1, 3, 16, 3),
+    # chunks
+    ([0], [40], 2, 6, 16, 0), ([0], [200], 1, 6, 64, 128), ([300], [70], 2, 6, 64, 128),
+    ([0, 130, 50], [33, 1, 129], 1, 8, 128, 64), ([37], [257], 1, 1, 16, 31), ([500], [90], 1, 16, 48, 1),
+    ([0, 20], [17, 300], 1, 5, 16, 128)]
+
+
+def _attend(hl, cb8, past, new, H, G, P, R, seed=0, scale=None, behind=2, max_new=None, spikes=True):
+    table, cu, slots, kv = _batch(past, new, H, P, R, seed, spikes)
+    T = sum(new)
+    Q = _rows(T, H * G, seed + 40, spikes=False)
+    state = [O.kv_paged_append(X, slots, cu, past, packed, norms, win.double().numpy(), R) for X, win, packed, norms in kv]
+    want, tol = O.kv_paged_attention(Q, cu, past, table, *state, R, 0.0625 if scale is None else scale)
+    # what attention must not read: pages of no request, places behind the last token, unused ring slots
+    used = np.zeros(kv[0][2].shape[0] * P, bool)
+    ring = np.zeros((len(past), max(R, 1)), bool)
+    for b, (p, n) in enumerate(zip(past, new)):
+        i = np.arange(O.kv_encoded(p + n, R))
+        used[table[b, i // P] * P + i % P] = True
+        if R:
+            ring[b, np.arange(O.kv_encoded(p + n, R), p + n) % R] = True
+    dev = []
+    for packed, norms, win in state:
+        norms = np.where(used.reshape(-1, 1, P), norms, np.float16(np.nan))
+        packed = np.where(used.reshape(-1, 1, P, 1), packed, np.uint8(255))
+        w = torch.from_numpy(win).to(torch.bfloat16).cuda() if R else None
+        if R:
+            w.transpose(1, 2)[torch.from_numpy(~ring[:, :R]).cuda()] = float("nan")
+        dev.append((_dev_pages(packed, norms), w))
+    Qd = torch.full((T + behind, H * G, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+    Qd[:T] = Q.cuda()
+    out = torch.full_like(Qd, 7.0)
+    args = (Qd, _ints(cu), _ints(past), _ints(table), dev[0][0], dev[1][0], (dev[0][1], dev[1][1]) if R else None, cb8,
+            max_new or max(new))
+    return args, dict(scale=scale, out=out), want, tol
+
+
+def _check(out, want, tol, T):
+    got = out[:T].double().cpu().numpy()
+    err = np.linalg.norm(got - want, axis=-1)
+    assert np.all(np.isfinite(got))
+    assert np.all(err <= tol), (np.max(err / tol), np.unravel_index(np.argmax(err / tol), err.shape))
+    assert torch.all(out[T:] == 7.0)   # rows behind the last request stay as they were
+
+
+@pytest.mark.parametrize("past,new,H,G,P,R", ATTENTIONS)
+def test_attention(hl, cb8, past, new, H, G, P, R):
+    args, kw, want, tol = _attend(hl, cb8, past, new, H, G, P, R, seed=sum(past) + R + G)
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    _check(out, want, tol, sum(new))
+    again = hl.kv_paged_attention(*args, scale=kw["scale"], out=torch.full_like(out, 7.0))
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)     # the same inputs give the same bits
+    assert hl.device_error() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.25, 1e-6])
+def test_attention_scales(hl, cb8, scale):
+    """A flat softmax, a sharp one (scores of some tens), a negative scale."""
+    for past, new in (([200], [1]), ([150], [40])):
+        args, kw, want, tol = _attend(hl, cb8, past, new, 2, 4, 16, 32, seed=9, scale=scale, spikes=False)
+        out = hl.kv_paged_attention(*args, **kw)
+        torch.cuda.synchronize()
+        _check(out, want, tol, sum(new))
+
+
+def test_attention_bound_on_new_tokens_may_be_loose(hl, cb8):
+    for max_new in (3, 8, 100, 1000):
+        args, kw, want, tol = _attend(hl, cb8, [60, 5], [1, 3], 1, 6, 16, 16, seed=4, max_new=max_new)
+        out = hl.kv_paged_attention(*args, **kw)
+        torch.cuda.synchronize()
+        _check(out, want, tol, 4)
+
+
+def test_attention_norms_of_very_different_size(hl, cb8):
+    """Value norms from 2^-20 to 2^14: small ones next to large ones neither
+    overflow nor vanish; each request has one magnitude in its output."""
+    args, kw, _, _ = _attend(hl, cb8, [100, 100, 100], [1, 1, 1], 1, 6, 16, 0, seed=3, spikes=False)
+    table = args[3].cpu().numpy()
+    for which, norms in ((0, args[4][1]), (1, args[5][1])):
+        n = norms.cpu().view(torch.float16).clone()
+        for b, e in enumerate((-18, 10, 0)):
+            for k in range(7):
+                n[int(table[b, k])] *= 2.0 ** e if which else 1.0
+        if which:
+            n[int(table[2, 0])] *= 2.0 ** -18
+            n[int(table[2, 5])] *= 2.0 ** 9
+        norms.copy_(n.view(torch.uint16).cuda())
+    state = [(p[0].cpu().numpy(), p[1].cpu().numpy().view(np.float16), np.zeros((3, 1, 0, 256))) for p in (args[4], args[5])]
+    for p, n, _ in state:   # the unused places: any finite value for the oracle, which does not read them
+        n[np.isnan(n)] = 0
+    want, tol = O.kv_paged_attention(args[0][:3].cpu(), args[1].tolist(), [100, 100, 100], table, *state, 0, 0.0625)
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    # norms below 2^-14 are subnormal binary16: exact as stored, the oracle reads the same
+    _check(out, want, tol, 3)
+
+
+def test_attention_with_strided_rows(hl, cb8):
+    """Q and out inside wider rows (a fused projection's output)."""
+    args, kw, want, tol = _attend(hl, cb8, [90, 10], [1, 20], 2, 3, 16, 16, seed=6)
+    T, Hq = args[0].shape[:2]
+    wide = torch.zeros(T, Hq + 4, 256, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:2 + Hq] = args[0]
+    res = torch.full((T, Hq + 1, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    hl.kv_paged_attention(wide[:, 2:2 + Hq], *args[1:], out=res[:, :Hq])
+    torch.cuda.synchronize()
+    _check(res[:, :Hq], want, tol, 21)
+    assert torch.all(res[:, Hq] == 7.0)
+
+
+def test_attention_leaves_out_pages_that_are_not_there(hl, cb8):
+    """Table entries outside the pool are reported and their keys left out."""
+    hl.device_error()
+    for new in (1, 40):
+        args, kw, _, _ = _attend(hl, cb8, [64], [new], 1, 6, 16, 0, seed=8)
+        table = args[3].clone()
+        table[0, 1], table[0, 3] = -1, args[4][0].shape[0]
+        out = hl.kv_paged_attention(*args[:3], table, *args[4:], **kw)
+        assert hl.device_error() == hl.DEVERR_KV_RANGE
+        # the same as without these pages' keys: the queries see the other ones
+        k, v = ((p[0].cpu().numpy(), p[1].cpu().numpy().view(np.float16)) for p in (args[4], args[5]))
+        t = args[3].cpu().numpy()[0]
+        i = np.array([i for i in range(64 + new) if i // 16 not in (1, 3)])
+        K, V = (O.kv_dequantize(p[t[i // 16], 0, i % 16], n[t[i // 16], 0, i % 16]) for p, n in (k, v))
+        for j in range(new):
+            for g in range(6):
+                seen = i <= 64 + j
+                s = K[seen] @ args[0][j, g].double().cpu().numpy() / 16
+                w = np.exp(s - s.max())
+                want = w / w.sum() @ V[seen]
+                got = out[j, g].double().cpu().numpy()
+                assert np.linalg.norm(got - want) <= 2.0 ** -6 * np.linalg.norm(want) + 2.0 ** -6
+
+
+def test_attention_rows_whose_every_page_is_gone(hl, cb8):
+    """No key left: the row is zero, and nothing is NaN."""
+    hl.device_error()
+    for new in (1, 30):
+        args, kw, _, _ = _attend(hl, cb8, [20], [new], 1, 4, 16, 0, seed=8)
+        out = hl.kv_paged_attention(*args[:3], torch.full_like(args[3], -1), *args[4:], **kw)
+        assert hl.device_error() == hl.DEVERR_KV_RANGE
+        assert torch.all(out[:new] == 0) and torch.all(out[new:] == 7.0)
+
+
+def test_attention_with_offsets_out_of_range(hl, cb8):
+    hl.device_error()
+    args, kw, want, tol = _attend(hl, cb8, [20, 30], [1, 1], 1, 4, 16, 0, seed=8)
+    T = args[0].shape[0]
+    for cu in ([0, 1, T + 1], [0, 5, 2], [-1, 1, 2]):
+        hl.kv_paged_attention(args[0], _ints(cu), *args[2:], **kw)
+        assert hl.device_error() & ~hl.DEVERR_KV_RANGE == 0
+    hl.kv_paged_attention(args[0], args[1], _ints([-1, 30]), *args[3:], **kw)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    _check(out, want, tol, 2)
+
+
+def test_attention_nan_stays_in_its_row(hl, cb8):
+    for past, new in (([40], [3]), ([40], [60])):
+        args, kw, want, tol = _attend(hl, cb8, past, new, 1, 4, 16, 8, seed=2)
+        args[0][1, 2, 7] = float("nan")
+        out = hl.kv_paged_attention(*args, **kw)
+        torch.cuda.synchronize()
+        assert torch.all(torch.isnan(out[1, 2]))
+        out[1, 2] = torch.from_numpy(want[1, 2]).to(out.dtype).cuda()
+        _check(out, want, tol, new[0])
+
+
+# ------------------------------------------------------------------ together
+def _reference(X, Y, Q, N, n, R, G):
+    """The last n queries of one request's N tokens, heads [N][H][256]."""
+    H = X.shape[1]
+    P = 16
+    pages = -(-N // P)
+    table, cu, slots, _ = O.kv_block_tables([0], [N], list(range(pages)), np.full((1, pages), -1), P, R, N)
+    st = [O.kv_paged_append(x, slots, cu, [0], np.zeros((pages, H, P, 96), np.uint8), np.zeros((pages, H, P), np.float16),
+                            np.zeros((1, H, R, 256)), R) for x in (X, Y)]
+    return O.kv_paged_attention(Q, [0, n], [N - n], table, *st, R, 0.0625)
+
+
+@pytest.mark.parametrize("R,P", [(16, 16), (0, 48), (128, 64)])
+def test_serving_run(hl, cb8, R, P):
+    """Requests that arrive, decode, verify drafts, leave and come back in rows
+    that had others before, all through the cache's public calls."""
+    H, G, B = 2, 3, 3
+    cache = hl.PagedKVCache(B, H, num_pages=40, max_pages=24, page_size=P, R=R, cb8=cb8)
+    story = [[30, 0, 0], [1, 50, 0], [1, 1, 7], [4, 1, 130], [0, 1, 1], "free 1", [1, 0, 1], [2, 33, 1], [1, 1, 1]]
+    seen = [[], [], []]
+    for k, new in enumerate(story):
+        if isinstance(new, str):
+            cache.release(1)
+            seen[1] = []
+            continue
+        T = sum(new)
+        K, V, Q = _rows(T + 3, H, 100 * k + 1), _rows(T + 3, H, 100 * k + 2), _rows(T + 3, H * G, 100 * k + 3, False)
+        cache.begin(_ints(new), T + 3)
+        cache.append(K.cuda(), V.cuda())
+        out = cache.attention(Q.cuda(), max(new), out=torch.full((T + 3, H * G, 256), 7.0, dtype=torch.bfloat16, device="cuda"))
+        cache.end()
+        torch.cuda.synchronize()
+        at = 0
+        for b, n in enumerate(new):
+            seen[b] += [(K[at + j], V[at + j]) for j in range(n)]
+            if n:
+                X, Y = (torch.stack([s[w] for s in seen[b]]) for w in (0, 1))
+                want, tol = _reference(X, Y, Q[at:at + n], len(seen[b]), n, R, G)
+                _check(torch.cat([out[at:at + n], out[T:]]), want, tol, n)
+            at += n
+    held = sum(O.kv_pages(len(s), P, R) for s in seen)
+    assert int(cache.n_free) == 40 - held
+    rest = cache.free_pages[:40 - held].tolist()
+    table = cache.block_table.cpu().numpy()
+    mine = [int(table[b, k]) for b in range(B) for k in range(O.kv_pages(len(seen[b]), P, R))]
+    assert sorted(rest + mine) == list(range(40))   # no page twice, none lost
+    assert hl.device_error() == 0
+
+
+@pytest.mark.parametrize("T,max_new", [(4, 1), (24, 20)])
+def test_step_in_a_graph(hl, cb8, T, max_new):
+    """One captured step, replayed with other lengths and inputs on another
+    stream, does what the eager calls do."""
+    H, G, B, R, P = 2, 6, 4, 8, 16
+
+    def cache():
+        return hl.PagedKVCache(B, H, num_pages=60, max_pages=20, page_size=P, R=R, cb8=cb8)
+
+    K, V, Q = (torch.zeros(T, n, 256, dtype=torch.bfloat16, device="cuda") for n in (H, H, H * G))
+    n_new, out = _ints([0] * B), torch.zeros(T, H * G, 256, dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(T, dtype=torch.int64, device="cuda")
+    a, b = cache(), cache()
+    ws = torch.empty(max(16, hl.kv_attention_workspace(Q, H, B, max_new)), dtype=torch.uint8, device="cuda")
+
+    def step(c, out):
+        c.begin(n_new, T, slot_map=slots)
+        c.append(K, V)
+        c.attention(Q, max_new, out=out, workspace=ws)
+        c.end()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(a, out)    # nothing yet: all lengths are 0
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step(a, out)
+    torch.cuda.current_stream().wait_stream(side)
+    step(b, out)
+    rng = np.random.default_rng(T)
+    for k in range(6):
+        new = rng.integers(0, max_new + 1, B)
+        new[3] = 0 if k == 2 else new[3]
+        while new.sum() > T:
+            new[int(np.argmax(new))] //= 2
+        n_new.copy_(_ints(new))
+        for x, h, s in ((K, H, 1), (V, H, 2), (Q, H * G, 3)):
+            x.copy_(_rows(T, h, 50 * k + s).cuda())
+        want = torch.full_like(out, 3.0)
+        out.fill_(3.0)
+        g.replay()
+        step(b, want)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), k
+        for x, y in ((a.n_past, b.n_past), (a.n_free, b.n_free), (a.block_table, b.block_table),
+                     (a.k_pages[0], b.k_pages[0]), (a.v_pages[1], b.v_pages[1]), (a.window[0], b.window[0])):
+            assert torch.equal(x, y), k
+    assert hl.device_error() == 0
+
+
+def test_long_cache_offsets(hl, cb8):
+    """Page offsets past 2^31 bytes: a pool of 2.6 GB whose last pages are used."""
+    H, P, G = 4, 4096, 6
+    n = 2 ** 31 // (H * P * 96) + 300
+    packed, norms = torch.zeros(n, H, P, 96, dtype=torch.uint8, device="cuda"), torch.zeros(n, H, P, dtype=torch.uint16, device="cuda")
+    T = 40
+    K, V = _rows(T, H, 1), _rows(T, H, 2)
+    Q = _rows(T, H * G, 3, False)
+    table = _ints([[n - 1]])
+    slots = _ints([(n - 1) * P + i for i in range(T)], torch.int64)
+    pages = (packed, norms)
+    vpages = (packed.clone(), norms.clone())
+    hl.kv_paged_append(K.cuda(), V.cuda(), slots, _ints([0, T]), _ints([0]), pages, vpages, None, cb8)
+    want, tol = _reference(K, V, Q, T, T, 0, G)
+    out = hl.kv_paged_attention(Q.cuda(), _ints([0, T]), _ints([0]), table, pages, vpages, None, cb8, T)
+    one = hl.kv_paged_attention(Q[-1:].cuda(), _ints([0, 1]), _ints([T - 1]), table, pages, vpages, None, cb8, 1)
+    torch.cuda.synchronize()
+    _check(out, want, tol, T)
+    _check(one, want[-1:], tol[-1:], 1)
