@@ -10,6 +10,7 @@
 // with y_j = n_j c[code_j] / 1 or v_j H: no cached vector is ever un-rotated.
 
 #include "kvpage.cuh"
+#include "sm100.cuh"
 
 namespace hlwq {
 
@@ -37,146 +38,786 @@ struct KvAttn {
   int64_t R;
 };
 
-constexpr int kAtHeads = 8;  // query heads of one kv head that a CTA takes
+// ---------------------------------------------------------------- the work, shared out
+//
+// An item is (request, row tile, kv head): a row tile is kRows consecutive
+// (token, query head) rows of a request, row = token * G + g.  An item's keys are
+// cut into units (64 encoded tokens, or kWinUnit window tokens); all items' units
+// in order, numbered 0 .. U - 1, are shared out evenly over the grid's CTAs in
+// contiguous ranges, whatever the requests' lengths are: one long request
+// is split over the machine, many short ones are not split.  Where a boundary
+// between two CTAs falls inside an item, its parts go to the workspace and
+// kv_attn_join_kernel adds them up.  Everything follows from cu and n_past, so every CTA
+// (and the join) works the shares out for itself: no plan is stored and the
+// host needs no lengths.
 
-// One CTA per (token, kv head, 8 query heads): 32 keys at a time, eight lanes
-// per key.
-__global__ void __launch_bounds__(256)
-kv_attn_simple_kernel(const KvAttn a) {
-  __shared__ __align__(16) float qs[kAtHeads * kKvQRow];
-  __shared__ float vt[32][kKvDim];
-  __shared__ float ss[kAtHeads][32];
-  __shared__ float m_run[kAtHeads], l_run[kAtHeads], corr[kAtHeads];
-  __shared__ float cb[kKvLevels];
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, g0 = blockIdx.z * kAtHeads, ng = min(kAtHeads, a.G - g0);
-  const int lane = threadIdx.x & 31, l8 = lane & 7, warp = threadIdx.x >> 5, grp = threadIdx.x >> 3;
-  kv_check_codebook(a.codebook);
-  const int b = kv_request_of(a.cu, a.B, t);
-  if (b < 0) return;
-  const int64_t c0 = __ldg(a.cu + b), n = __ldg(a.cu + b + 1) - c0, p = __ldg(a.n_past + b);
-  if (c0 < 0 || c0 > t || t >= c0 + n || c0 + n > a.T || p < 0) {
-    if (threadIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
-    return;
+constexpr int kUnit = 64;     // encoded tokens per unit
+constexpr int kWinUnit = 32;  // window tokens per unit (they are rotated here: about twice the work per token)
+
+constexpr int64_t kMaxKeys = INT32_MAX - 4096;  // key positions are 32-bit below
+
+struct KvItem {
+  int b;            // request
+  int64_t c0, n;    // its first row of Q and its new tokens
+  int64_t p;        // cached tokens before the step
+  int64_t row0;     // first row of the tile, rows of the request in all: n * G
+  int64_t n_enc;    // encoded tokens of the request
+  int64_t e_lim;    // encoded tokens that the tile's last row sees
+  int64_t w_lim;    // tokens that it sees, window included
+  int e_units, units;
+};
+
+// The pair (request, row tile) number `pair`; units = 0 where it has no rows.
+template <int kRows>
+__device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, bool& bad) {
+  KvItem it;
+  it.b = pair / tiles;
+  const int rt = pair - it.b * tiles;
+  it.c0 = __ldg(a.cu + it.b);
+  it.n = __ldg(a.cu + it.b + 1) - it.c0;
+  it.p = __ldg(a.n_past + it.b);
+  it.row0 = static_cast<int64_t>(rt) * kRows;
+  it.units = 0;
+  it.e_units = 0;
+  if (it.c0 < 0 || it.n < 0 || it.c0 + it.n > a.T || it.p < 0 || it.p + it.n > kMaxKeys) {
+    bad = true;
+    it.n = 0;
   }
-  const int64_t n_enc = kv_enc(p + n, a.R), keys = p + (t - c0) + 1;
-  if (threadIdx.x < kKvLevels) cb[threadIdx.x] = __ldg(a.codebook + threadIdx.x);
-  if (threadIdx.x < kAtHeads) m_run[threadIdx.x] = -3.0e38f, l_run[threadIdx.x] = 0.0f;
-  for (int m = warp * 4; m < ng; m += 32) {
-    const int g = m + (lane >> 3);
-    const bool on = g < ng;
-    float v[32];
-    const uint16_t* src = a.q + t * a.ldq + (h * a.G + g0 + (on ? g : 0)) * kKvDim + 32 * l8;
+  const int64_t rows = it.n * a.G;
+  if (rt == 0 && rows > static_cast<int64_t>(tiles) * kRows) bad = true;  // more than max_new tokens
+  if (it.row0 >= rows) return it;
+  const int64_t last = (min(it.row0 + kRows, rows) - 1) / a.G;  // the tile's last token
+  const int64_t sees = it.p + last + 1;
+  it.n_enc = kv_enc(it.p + it.n, a.R);
+  it.e_lim = min(it.n_enc, sees);
+  it.w_lim = sees;
+  it.e_units = static_cast<int>(ceil_div(it.e_lim, kUnit));
+  it.units = it.e_units + static_cast<int>(ceil_div(it.w_lim - it.e_lim, kWinUnit));
+  return it;
+}
+
+// The total of all units, and where `want` (0 <= want < U) lies: its pair and the
+// pair's first unit.  Called by all kThreads threads of the CTA with the same arguments.
+template <int kRows, int kThreads>
+__device__ __forceinline__ int64_t kv_total_units(const KvAttn& a, int tiles, int64_t* warp_sums, int64_t& mine0) {
+  const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int pair = threadIdx.x * per + i;
+    if (pair < pairs) sum += static_cast<int64_t>(kv_item<kRows>(a, pair, tiles, bad).units) * a.H;
+  }
+  if (bad && blockIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+  int64_t inc = sum;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = bf16_bits_to_float(__ldg(src + e));
-    kv_fwht(v, lane);
-    if (on) {
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) qs[kv_qpos(g, 32 * l8 + e)] = v[e] * (a.scale / 256.0f);
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+  mine0 = before + inc - sum;
+  return total;
+}
+
+// After kv_total_units: the pair holding unit `want`, found by the thread whose
+// pairs contain it and published in found[0] (pair) and found[1] (its first unit).
+template <int kRows, int kThreads>
+__device__ __forceinline__ void kv_find_unit(const KvAttn& a, int tiles, int64_t mine0, int64_t want, int64_t* found) {
+  const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
+  int64_t u = mine0;
+  bool bad = false;
+  if (u <= want) {
+    for (int i = 0; i < per; ++i) {
+      const int pair = threadIdx.x * per + i;
+      if (pair >= pairs) break;
+      const int64_t n = static_cast<int64_t>(kv_item<kRows>(a, pair, tiles, bad).units) * a.H;
+      if (want < u + n) {
+        found[0] = pair;
+        found[1] = u;
+        break;
+      }
+      u += n;
     }
   }
   __syncthreads();
-  float acc[kAtHeads];
+}
+
+__device__ __forceinline__ int64_t kv_share(int64_t U, int c, int ctas) { return U * c / ctas; }
+
+// ---------------------------------------------------------------- building blocks
+
+// 2^k that brings a row's largest magnitude (>= 0) into [16, 32); 1 for a zero row.
+__device__ __forceinline__ float pow2_scale(float mx, float& inv) {
+  const int e = static_cast<int>(__float_as_uint(mx) >> 23);
+  const int k = e == 0 ? 0 : max(-120, min(120, 131 - e));
+  inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float oct_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+}
+
+__device__ __forceinline__ void load_bf16x32(float (&v)[32], const uint16_t* src, bool on) {
 #pragma unroll
-  for (int g = 0; g < kAtHeads; ++g) acc[g] = 0.0f;
-  for (int64_t r0 = 0; r0 < keys; r0 += 32) {
-    const int64_t r = r0 + grp;
-    const bool on = r < keys, coded = on && r < n_enc;
-    int64_t row = -1;
-    if (coded) {
-      const int64_t k = r / a.P;
-      const int page = k < a.max_pages ? __ldg(a.table + b * a.max_pages + k) : -1;
-      if (page < 0 || page >= a.num_pages) raise_device_error(HLWQ_DEVERR_KV_RANGE);
-      else row = (static_cast<int64_t>(page) * a.H + h) * a.P + r % a.P;
-    }
-    const bool live = on && (!coded || row >= 0);
-    for (int kv = 0; kv < 2; ++kv) {
-      float v[32];
-      float sc = 0.0f;
+  for (int c = 0; c < 4; ++c) {
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (on) u = __ldg(reinterpret_cast<const uint4*>(src) + c);
+    const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-      if (on && !coded) {
-        const uint16_t* src = (kv ? a.vwin : a.kwin) + ((static_cast<int64_t>(b) * a.H + h) * a.R + r % a.R) * kKvDim + 32 * l8;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = bf16_bits_to_float(__ldg(src + e));
-        sc = 1.0f;
-      }
-      kv_fwht(v, lane);
-      if (row >= 0) {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>((kv ? a.vp : a.kp) + row * kKvBytes + 12 * l8);
-        const uint32_t w[3] = {__ldg(src), __ldg(src + 1), __ldg(src + 2)};
-        sc = half_bits_to_float(__ldg((kv ? a.vn : a.kn) + row));
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = cb[kv_code(w, e)];
-      }
-      if (kv == 0) {
-        for (int g = 0; g < ng; ++g) {
-          float d = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) d = fmaf(v[e], qs[kv_qpos(g, 32 * l8 + e)], d);
-          d = oct_sum(d);
-          if (l8 == 0) ss[g][grp] = live ? d * sc : -INFINITY;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) vt[grp][32 * l8 + e] = live ? v[e] * sc : 0.0f;
-      }
-    }
-    __syncthreads();
-    for (int g = warp; g < ng; g += 8) {
-      const float s = ss[g][lane];
-      float m = s;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = fmaxf(m, m_run[g]);
-      float e = expf(s - m);
-      ss[g][lane] = e;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
-      if (lane == 0) {
-        corr[g] = expf(m_run[g] - m);
-        l_run[g] = l_run[g] * corr[g] + e;
-        m_run[g] = m;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int g = 0; g < kAtHeads; ++g)
-      if (g < ng) {
-        float s = acc[g] * corr[g];
-        for (int k = 0; k < 32; ++k) s = fmaf(ss[g][k], vt[k][threadIdx.x], s);
-        acc[g] = s;
-      }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int g = 0; g < kAtHeads; ++g)
-    if (g < ng) qs[kv_qpos(g, threadIdx.x)] = acc[g];
-  __syncthreads();
-  for (int m = warp * 4; m < ng; m += 32) {
-    const int g = m + (lane >> 3);
-    const bool on = g < ng;
-    float v[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = qs[kv_qpos(on ? g : 0, 32 * l8 + e)];
-    kv_fwht(v, lane);
-    if (on) {
-      const float inv = l_run[g] > 0.0f ? 1.0f / (256.0f * l_run[g]) : l_run[g];
-      uint16_t* dst = a.out + t * a.ldo + (h * a.G + g0 + g) * kKvDim + 32 * l8;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) dst[e] = static_cast<uint16_t>(float_to_bf16_bits(v[e] * inv));
+    for (int k = 0; k < 4; ++k) {
+      v[8 * c + 2 * k] = bf16x2_lo(wd[k]);
+      v[8 * c + 2 * k + 1] = bf16x2_hi(wd[k]);
     }
   }
 }
 
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------- few rows per kv head
+//
+// At most 16 (token, head) rows per kv head: single tokens, a few drafted ones.
+// The codes are decoded into the registers of matrix instructions and nowhere else.
+//
+// S^T = K q^T with m16n8k16: A = 16 keys x 16 dims, B = 8 rows of q.  The
+// contraction's dims may come in any order, so lane (g, t) = (lane / 4, lane % 4)
+// takes dims 64 t + 4 s .. + 3 of keys g and g + 8 in step s: 24 contiguous bytes of each
+// key.  O^T = V^T P^T: A = 16 dims x 16 keys; its pairs run along keys 2t, 2t + 1
+// (and + 8), its rows are dims 32 g + 2 m and 32 g + 2 m + 1 of tile m, so a lane
+// takes 12 contiguous bytes of four keys.  Two 3-bit codes index a table of 64
+// binary16 pairs, one copy per lane (its own bank): two neighbouring codes of a
+// key, or the same code of two keys (the even and odd 3-bit fields of two words
+// are brought together with one select).  That is one table load and two integer
+// instructions for two values.
+//
+// P^T comes out of S^T's registers by two 8 x 8 transposes; row sums and maxima
+// stay in the lane until the end.  The running reference of a row's maximum is
+// raised only when a score exceeds it by 2^8 (exp2 stays below 2^8): the
+// sums are the same, most steps need no exchange between lanes.  A value's norm
+// rides on p; p n is kept in binary16's range by a power of two that follows the
+// largest norm (fv), so neither overflows and what is lost is 2^-39 of the
+// largest.  O^T's registers hold 32 consecutive dims of two rows: the final
+// rotation is five in-register and three shuffle stages.
+
+constexpr int kRowWarps = 4;
+constexpr int kRowThreads = 32 * kRowWarps;
+constexpr int kStage = 3136;  // 16 keys: K codes 1536, V codes 1536, K norms 32, V norms 32
+constexpr int kStages = 4;
+constexpr int kTabBytes = 64 * 128;
+constexpr float kMinM = -3.402823466e38f;
+
+template <int NT>
+struct RowCfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kQFrag = NT * 16 * 32 * 8;
+  static constexpr int kBuf = kStages * kStage;                  // per warp: ring, window tile, or 32 NT x 64 partial sums
+  static constexpr int kMerge = NT * 32 * 32 * 8;                // bytes of a warp's O
+  static constexpr int kWarpBytes = kBuf > kMerge ? kBuf : kMerge;
+  static constexpr int kSmem = 8192 /*align*/ + kTabBytes + kQFrag + kRowWarps * kWarpBytes;
+  static constexpr int kPart = kRows * (kKvDim + 2);             // floats of one partial result
+  static constexpr int kCtas = NT == 1 ? 3 : 2;                  // resident per SM
+};
+
+// Adds 16 keys' values to O: codes of four keys in w[4][3].
+template <int NT>
+__device__ __forceinline__ void rows_pv(float (&o)[NT][16][4], const uint32_t (&w)[4][3], uint32_t tab,
+                                        const uint32_t (&b)[NT][2]) {
+  constexpr uint32_t kEven = 0x071c71c7u;  // bits 6f .. 6f + 2
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {            // ten codes at a time, the last two
+    uint32_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = c == 0 ? w[k][0] : c == 1 ? __funnelshift_r(w[k][0], w[k][1], 30)
+                                       : c == 2 ? __funnelshift_r(w[k][1], w[k][2], 28) : w[k][2] >> 26;
+    uint32_t pr[2][2];  // [key pair][even / odd code]
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      pr[k][0] = (x[2 * k] & kEven) | ((x[2 * k + 1] << 3) & ~kEven);
+      pr[k][1] = ((x[2 * k] >> 3) & kEven) | (x[2 * k + 1] & ~kEven);
+    }
+#pragma unroll
+    for (int f = 0; f < (c == 3 ? 1 : 5); ++f) {
+      uint32_t a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // a0, a1: even and odd dim of the first key pair; a2, a3 of the second
+        const uint32_t v = pr[k >> 1][k & 1];
+        const uint32_t i = f == 0 ? v << 7 : f == 1 ? v << 1 : v >> (6 * f - 7);
+        a[k] = lds32((i & 0x1f80u) | tab);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][5 * c + f], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+    }
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kRowThreads, RowCfg<NT>::kCtas)
+kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
+  using C = RowCfg<NT>;
+  extern __shared__ __align__(16) uint8_t rsm_raw[];
+  __shared__ int64_t warp_sums[kRowWarps], found[2];
+  __shared__ float qmul[C::kRows];
+  __shared__ float mstat[kRowWarps][C::kRows], lstat[kRowWarps][C::kRows];
+  pdl_trigger();  // the join may be set up; it waits for this grid's results
+  const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(rsm_raw));
+  const uint32_t tab0 = (raw + 8191u) & ~8191u;  // 8 KB aligned: indices are or-ed in
+  uint8_t* gtab = rsm_raw + (tab0 - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, l8 = lane & 7;
+  const uint32_t qfrag = tab0 + kTabBytes, wbuf = qfrag + C::kQFrag + warp * C::kWarpBytes;
+  uint8_t* gbuf = gtab + (wbuf - tab0);
+  const uint32_t tab = tab0 + 4 * lane;
+  const int page_size = static_cast<int>(a.P);
+
+  kv_check_codebook(a.codebook);
+  for (int i = threadIdx.x; i < 64 * 32; i += kRowThreads)
+    reinterpret_cast<uint32_t*>(gtab)[i] = pack_half2(__ldg(a.codebook + ((i >> 5) & 7)), __ldg(a.codebook + (i >> 8)));
+
+  int64_t mine0;
+  const int64_t U = kv_total_units<C::kRows, kRowThreads>(a, tiles, warp_sums, mine0);
+  const int64_t u0 = kv_share(U, blockIdx.x, gridDim.x), u1 = kv_share(U, blockIdx.x + 1, gridDim.x);
+  if (u0 >= u1) return;
+  kv_find_unit<C::kRows, kRowThreads>(a, tiles, mine0, u0, found);
+  int pair = static_cast<int>(found[0]);
+  int64_t at = found[1];  // first unit of the pair
+  bool bad = false;
+  KvItem it = kv_item<C::kRows>(a, pair, tiles, bad);
+
+  for (int64_t u = u0; u < u1;) {
+    while (u >= at + static_cast<int64_t>(it.units) * a.H) {
+      at += static_cast<int64_t>(it.units) * a.H;
+      it = kv_item<C::kRows>(a, ++pair, tiles, bad);
+    }
+    const int h = static_cast<int>((u - at) / it.units);
+    const int ta = static_cast<int>(u - at - static_cast<int64_t>(h) * it.units);
+    const int tb = static_cast<int>(min(static_cast<int64_t>(it.units), ta + (u1 - u)));
+    u += tb - ta;
+    const int nrows = static_cast<int>(min(static_cast<int64_t>(C::kRows), it.n * a.G - it.row0));
+
+    // rotate the tile's rows into matrix-instruction order
+    for (int r0 = warp * 4; r0 < C::kRows; r0 += kRowWarps * 4) {
+      const int r = r0 + (lane >> 3);
+      const bool on = r < nrows;
+      const int64_t row = it.row0 + (on ? r : 0), tok = row / a.G;
+      float v[32];
+      load_bf16x32(v, a.q + (it.c0 + tok) * a.ldq + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * l8, on);
+      kv_fwht(v, lane);
+      float mx = 0.0f, inv;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
+      const float sc = pow2_scale(oct_max(mx), inv);
+      if (l8 == 0) qmul[r] = inv * a.scale * (1.4426950408889634f / 256.0f);
+      const uint32_t dst = qfrag + ((r >> 3) * 16 * 32 + (r & 7) * 4 + (l8 >> 1)) * 8 + (l8 & 1) * 8 * 256;
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + s * 256),
+                     "r"(pack_half2(v[4 * s] * sc, v[4 * s + 1] * sc)),
+                     "r"(pack_half2(v[4 * s + 2] * sc, v[4 * s + 3] * sc))
+                     : "memory");
+    }
+    __syncthreads();
+
+    float o[NT][16][4], m[NT][2], l[NT][2], qm[NT][2];
+    int lim[NT][2];
+    float fv = 2147483648.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = 8 * nt + 2 * t4 + k;
+        m[nt][k] = kMinM;
+        l[nt][k] = 0.0f;
+        qm[nt][k] = qmul[r];
+        lim[nt][k] = r < nrows ? static_cast<int>(it.p + (it.row0 + r) / a.G + 1) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[nt][i][k] = o[nt][i][2 + k] = 0.0f;
+      }
+
+    // scores of 16 keys (d, per row tile) -> the operand of P V
+    auto softmax = [&](float (&d)[NT][4], float nk0, float nk1, float nv0, float nv1, int key, int end,
+                       uint32_t(&b)[NT][2]) {
+      // key: index of this lane's first key; the second one is 8 further; keys from `end` on are not there
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int see = min(lim[nt][k], end);
+          d[nt][k] = key < see ? d[nt][k] * (nk0 * qm[nt][k]) : -INFINITY;
+          d[nt][2 + k] = key + 8 < see ? d[nt][2 + k] * (nk1 * qm[nt][k]) : -INFINITY;
+          over |= fmaxf(d[nt][k], d[nt][2 + k]) > m[nt][k] + 8.0f;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float x = fmaxf(fmaxf(d[nt][k], d[nt][2 + k]), m[nt][k]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float f = exp2f(m[nt][k] - x);
+            m[nt][k] = x;
+            l[nt][k] *= f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              o[nt][i][k] *= f;
+              o[nt][i][2 + k] *= f;
+            }
+          }
+      }
+      if (__any_sync(0xffffffffu, fmaxf(nv0, nv1) * fv > 128.0f)) {
+        float x = fmaxf(nv0, nv1);
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
+        const int e = min(144, static_cast<int>(__float_as_uint(x) >> 23) + 1);  // x < 2^(e - 127)
+        const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23), f = nf / fv;  // x nf in [16, 32)
+        fv = nf;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
+      }
+      const float f0 = nv0 * fv, f1 = nv1 * fv;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = exp2f(d[nt][k] - m[nt][k & 1]);
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
+        // a key that is masked out has no say, whatever its norm is
+        b[nt][0] = transpose_8x8(pack_half2(p[0] > 0.0f || p[0] != p[0] ? p[0] * f0 : 0.0f, p[1] > 0.0f || p[1] != p[1] ? p[1] * f0 : 0.0f));
+        b[nt][1] = transpose_8x8(pack_half2(p[2] > 0.0f || p[2] != p[2] ? p[2] * f1 : 0.0f, p[3] > 0.0f || p[3] != p[3] ? p[3] * f1 : 0.0f));
+      }
+    };
+
+    // ---- encoded keys: tiles of 16, one warp each, kStages - 1 of them under way
+    const int e_tb = min(tb, it.e_units);
+    const int k_end = static_cast<int>(min(static_cast<int64_t>(e_tb) * kUnit, it.e_lim));
+    const int k_first = ta * kUnit + 16 * warp;
+    auto request = [&](int k0, int stage) {  // false: the page is not there
+      bool there = false;
+      if (k0 < k_end) {
+        const int kp = k0 / page_size;
+        const int page = kp < a.max_pages ? __ldg(a.table + it.b * a.max_pages + kp) : -1;
+        if (page < 0 || page >= a.num_pages) {
+          if (lane == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+        } else {
+          there = true;
+          const int64_t row = (static_cast<int64_t>(page) * a.H + h) * a.P + (k0 - kp * page_size);
+          const uint32_t dst = wbuf + stage * kStage;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            cp_async16(dst + 16 * (lane + 32 * i), a.kp + row * kKvBytes + 16 * (lane + 32 * i));
+            cp_async16(dst + 1536 + 16 * (lane + 32 * i), a.vp + row * kKvBytes + 16 * (lane + 32 * i));
+          }
+          if (lane < 8) cp_async4(dst + 3072 + 4 * lane, a.kn + row + 2 * lane);
+          else if (lane < 16) cp_async4(dst + 3072 + 4 * lane, a.vn + row + 2 * (lane - 8));
+        }
+      }
+      cp_async_commit();
+      return there;
+    };
+    if (ta < e_tb) {
+      uint32_t there = 0;  // bit i: the tile in stage i may be read
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) there |= static_cast<uint32_t>(request(k_first + 64 * i, i)) << i;
+      int stage = 0;
+      for (int k0 = k_first; k0 < k_end; k0 += 64) {
+        const int ns = (stage + kStages - 1) % kStages;
+        __syncwarp();  // the stage is refilled: every lane has read it
+        there = (there & ~(1u << ns)) | static_cast<uint32_t>(request(k0 + 64 * (kStages - 1), ns)) << ns;
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        if ((there >> stage) & 1u) {
+          const uint32_t st = wbuf + stage * kStage;
+          const uint32_t nkw = lds32(st + 3072 + 4 * (g >> 1)), nkw2 = lds32(st + 3088 + 4 * (g >> 1));
+          const uint32_t nvw = lds32(st + 3104 + 4 * (g >> 1)), nvw2 = lds32(st + 3120 + 4 * (g >> 1));
+          const int ns16 = (g & 1) * 16;
+          uint32_t w0[6], w1[6];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint2 x = lds64(st + g * kKvBytes + 24 * t4 + 8 * i), y = lds64(st + (g + 8) * kKvBytes + 24 * t4 + 8 * i);
+            w0[2 * i] = x.x, w0[2 * i + 1] = x.y;
+            w1[2 * i] = y.x, w1[2 * i + 1] = y.y;
+          }
+          float d[2][NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[0][nt][k] = d[1][nt][k] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < 16; ++s) {
+            uint32_t af[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int bit = 12 * s + 6 * k, wi = bit >> 5, sh = bit & 31;
+              uint32_t x, y;
+              if (sh > 26) x = __funnelshift_r(w0[wi], w0[wi + 1], sh - 7), y = __funnelshift_r(w1[wi], w1[wi + 1], sh - 7);
+              else if (sh >= 7) x = w0[wi] >> (sh - 7), y = w1[wi] >> (sh - 7);
+              else x = w0[wi] << (7 - sh), y = w1[wi] << (7 - sh);
+              af[2 * k] = lds32((x & 0x1f80u) | tab);
+              af[2 * k + 1] = lds32((y & 0x1f80u) | tab);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q = lds64(qfrag + ((nt * 16 + s) * 32 + lane) * 8);
+              mma_16816(d[s & 1][nt], af[0], af[1], af[2], af[3], q.x, q.y);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[0][nt][k] += d[1][nt][k];
+          uint32_t b[NT][2];
+          softmax(d[0], half_bits_to_float(static_cast<uint16_t>(nkw >> ns16)),
+                  half_bits_to_float(static_cast<uint16_t>(nkw2 >> ns16)),
+                  half_bits_to_float(static_cast<uint16_t>(nvw >> ns16)),
+                  half_bits_to_float(static_cast<uint16_t>(nvw2 >> ns16)), k0 + g, k_end, b);
+          uint32_t vw[4][3];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              vw[k][i] = lds32(st + 1536 + (2 * t4 + (k & 1) + 8 * (k >> 1)) * kKvBytes + 12 * g + 4 * i);
+          rows_pv<NT>(o, vw, tab, b);
+        }
+        stage = (stage + 1) % kStages;
+      }
+      cp_async_wait<0>();
+      __syncwarp();
+    }
+
+    // ---- window keys, 16 at a time: rotated by eight lanes per vector into the
+    // warp's buffer as binary16 with a power-of-two scale in the norm's place
+    const int w_first = static_cast<int>(it.e_lim) + (max(ta, it.e_units) - it.e_units) * kWinUnit;
+    const int w_end = min(static_cast<int>(it.e_lim) + (tb - it.e_units) * kWinUnit, static_cast<int>(it.w_lim));
+    for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {
+      float nrm[2][2];  // [K, V][keys g, g + 8]
+      float d[NT][4];
+      uint32_t b[NT][2];
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        __syncwarp();
+        float* scales = reinterpret_cast<float*>(gbuf + 16 * 520);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int key = 4 * i + (lane >> 3);
+          const bool on = k0 + key < w_end;
+          float v[32];
+          load_bf16x32(v, (kv ? a.vwin : a.kwin) + ((static_cast<int64_t>(it.b) * a.H + h) * a.R + (on ? (k0 + key) % static_cast<int>(a.R) : 0)) * kKvDim + 32 * l8, on);
+          kv_fwht(v, lane);
+          float mx = 0.0f, inv;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
+          const float sc = pow2_scale(oct_max(mx), inv);
+          if (l8 == 0) scales[key] = inv;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint2*>(gbuf + key * 520 + 64 * l8 + 8 * e) =
+                make_uint2(pack_half2(v[4 * e] * sc, v[4 * e + 1] * sc), pack_half2(v[4 * e + 2] * sc, v[4 * e + 3] * sc));
+        }
+        __syncwarp();
+        nrm[kv][0] = scales[g];
+        nrm[kv][1] = scales[g + 8];
+        if (kv == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < 16; ++s) {
+            const uint2 x = lds64(wbuf + g * 520 + 128 * t4 + 8 * s), y = lds64(wbuf + (g + 8) * 520 + 128 * t4 + 8 * s);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q = lds64(qfrag + ((nt * 16 + s) * 32 + lane) * 8);
+              mma_16816(d[nt], x.x, y.x, x.y, y.y, q.x, q.y);
+            }
+          }
+        }
+      }
+      softmax(d, nrm[0][0], nrm[0][1], nrm[1][0], nrm[1][1], k0 + g, w_end, b);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = lds32(wbuf + (2 * t4 + (k & 1) + 8 * (k >> 1)) * 520 + 64 * g + 4 * i);
+        const uint32_t a0 = __byte_perm(x[0], x[1], 0x5410), a1 = __byte_perm(x[0], x[1], 0x7632);
+        const uint32_t a2 = __byte_perm(x[2], x[3], 0x5410), a3 = __byte_perm(x[2], x[3], 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+      }
+    }
+
+    // ---- the four warps' results: common maximum, sums, and O
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 4);
+        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 8);
+        l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 16);
+        if (g == 0) {
+          mstat[warp][8 * nt + 2 * t4 + k] = m[nt][k];
+          lstat[warp][8 * nt + 2 * t4 + k] = l[nt][k];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = 8 * nt + 2 * t4 + k;
+        float x = mstat[0][r];
+#pragma unroll
+        for (int w = 1; w < kRowWarps; ++w) x = fmaxf(x, mstat[w][r]);
+        const float f = exp2f(m[nt][k] - x) / fv;
+        // [row tile][row parity][tile m, dim parity][lane]
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float* dst = reinterpret_cast<float*>(gbuf) + ((nt * 2 + k) * 32 + 2 * i) * 32 + lane;
+          dst[0] = o[nt][i][k] * f;
+          dst[32] = o[nt][i][2 + k] * f;
+        }
+      }
+    __syncthreads();
+    if (warp < 2 * NT) {
+      // this warp: rows 8 nt + 2 t + k of its (nt, k) = (warp / 2, warp % 2)
+      const int r = 8 * (warp >> 1) + 2 * t4 + (warp & 1);
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        const float* src = reinterpret_cast<const float*>(gtab + (qfrag + C::kQFrag - tab0) + w * C::kWarpBytes) + warp * 1024 + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += src[32 * i];
+      }
+      float mx = mstat[0][r], sum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < kRowWarps; ++w) mx = fmaxf(mx, mstat[w][r]);
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) sum += lstat[w][r] * exp2f(mstat[w][r] - mx);
+      if (ta == 0 && tb == it.units) {
+        kv_stage<float, 1>(v);
+        kv_stage<float, 2>(v);
+        kv_stage<float, 4>(v);
+        kv_stage<float, 8>(v);
+        kv_stage<float, 16>(v);
+        kv_stage_x<float, 4>(v, lane);
+        kv_stage_x<float, 8>(v, lane);
+        kv_stage_x<float, 16>(v, lane);
+        if (r < nrows) {
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / (256.0f * sum);
+          const int64_t row = it.row0 + r, tok = row / a.G;
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (it.c0 + tok) * a.ldo + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * g);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 x;
+            x.x = float_to_bf16_bits(v[8 * c] * inv) | (float_to_bf16_bits(v[8 * c + 1] * inv) << 16);
+            x.y = float_to_bf16_bits(v[8 * c + 2] * inv) | (float_to_bf16_bits(v[8 * c + 3] * inv) << 16);
+            x.z = float_to_bf16_bits(v[8 * c + 4] * inv) | (float_to_bf16_bits(v[8 * c + 5] * inv) << 16);
+            x.w = float_to_bf16_bits(v[8 * c + 6] * inv) | (float_to_bf16_bits(v[8 * c + 7] * inv) << 16);
+            dst[c] = x;
+          }
+        }
+      } else {
+        float* part = parts + static_cast<int64_t>(2 * blockIdx.x + (ta == 0 ? 1 : 0)) * C::kPart;
+        float4* dst = reinterpret_cast<float4*>(part + r * kKvDim + 32 * g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        if (g == 0) {
+          part[C::kRows * kKvDim + r] = mx;
+          part[C::kRows * (kKvDim + 1) + r] = sum;
+        }
+      }
+    }
+    __syncthreads();  // the buffers and the statistics are free for the next item
+  }
+}
+
+// Adds the parts of the items that a boundary between CTAs cut: CTA (c, row)
+// joins that row of the item in which boundary c (before CTA c of the attention
+// grid of `ctas`) is the first one.  Eight warps take the parts in turn, each
+// lane eight dims; then one warp rotates and writes the row.
+constexpr int kJoinThreads = 256;
+template <int kRows>
+__global__ void __launch_bounds__(kJoinThreads)
+kv_attn_join_kernel(const KvAttn a, int tiles, int ctas, const float* __restrict__ parts) {
+  __shared__ int64_t warp_sums[kJoinThreads / 32], found[2];
+  __shared__ float acc[kJoinThreads / 32][kKvDim], ms[kJoinThreads / 32], ls[kJoinThreads / 32];
+  constexpr int kPart = kRows * (kKvDim + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, c = blockIdx.x + 1;
+  int64_t mine0;
+  const int64_t U = kv_total_units<kRows, kJoinThreads>(a, tiles, warp_sums, mine0);
+  const int64_t uc = kv_share(U, c, ctas), ub = kv_share(U, c - 1, ctas);
+  pdl_wait();  // in every CTA: the join has not ended before the attention has
+  if (uc >= U || uc == ub) return;
+  kv_find_unit<kRows, kJoinThreads>(a, tiles, mine0, uc, found);
+  bool bad = false;
+  const KvItem it = kv_item<kRows>(a, static_cast<int>(found[0]), tiles, bad);
+  const int h = static_cast<int>((uc - found[1]) / it.units);
+  const int64_t s0 = found[1] + static_cast<int64_t>(h) * it.units, s1 = s0 + it.units;
+  if (uc == s0 || ub > s0) return;  // no cut, or not its first
+  if (it.row0 + r >= it.n * a.G) return;
+  float v[8];
+  float m = kMinM, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  // part 0 is CTA c - 1's, part j >= 1 CTA c + j - 1's
+  int count = 1;
+  for (int k = c; k < ctas && kv_share(U, k, ctas) < s1; ++k) ++count;
+  for (int j = warp; j < count; j += kJoinThreads / 32) {
+    const int k = c - 1 + j;
+    if (kv_share(U, k, ctas) == kv_share(U, k + 1, ctas)) continue;
+    const float* part = parts + static_cast<int64_t>(2 * k + (j == 0 ? 1 : 0)) * kPart;
+    const float pm = part[kRows * kKvDim + r], pl = part[kRows * (kKvDim + 1) + r];
+    const float4 x = reinterpret_cast<const float4*>(part + r * kKvDim)[2 * lane];
+    const float4 y = reinterpret_cast<const float4*>(part + r * kKvDim)[2 * lane + 1];
+    const float nm = fmaxf(m, pm), fo = exp2f(m - nm), fn = exp2f(pm - nm);
+    m = nm;
+    l = l * fo + pl * fn;
+    const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * fo + w[i] * fn;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[warp][8 * lane + i] = v[i];
+  if (lane == 0) ms[warp] = m, ls[warp] = l;
+  __syncthreads();
+  if (warp) return;
+  for (int w = 1; w < kJoinThreads / 32; ++w) {
+    const float nm = fmaxf(m, ms[w]), fo = exp2f(m - nm), fn = exp2f(ms[w] - nm);
+    m = nm;
+    l = l * fo + ls[w] * fn;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * fo + acc[w][8 * lane + i] * fn;
+  }
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & s) == 0) {
+        const float x = v[i], y = v[i + s];
+        v[i] = x + y;
+        v[i + s] = x - y;
+      }
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = __shfl_xor_sync(0xffffffffu, v[i], s);
+      v[i] = (lane & s) ? x - v[i] : v[i] + x;
+    }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / (256.0f * l);
+  const int64_t row = it.row0 + r, tok = row / a.G;
+  uint4 x;
+  x.x = float_to_bf16_bits(v[0] * inv) | (float_to_bf16_bits(v[1] * inv) << 16);
+  x.y = float_to_bf16_bits(v[2] * inv) | (float_to_bf16_bits(v[3] * inv) << 16);
+  x.z = float_to_bf16_bits(v[4] * inv) | (float_to_bf16_bits(v[5] * inv) << 16);
+  x.w = float_to_bf16_bits(v[6] * inv) | (float_to_bf16_bits(v[7] * inv) << 16);
+  reinterpret_cast<uint4*>(a.out + (it.c0 + tok) * a.ldo + (h * a.G + (row - tok * a.G)) * kKvDim)[lane] = x;
+}
+
+// The attention grid and its row tiles for max_new new tokens of a request.
+struct KvGrid {
+  int rows, ctas, tiles;
+};
+inline KvGrid kv_grid(int64_t max_new, int64_t G) {
+  const int rows = max_new * G <= 8 ? 8 : 16;
+  return {rows, sm_count() * (rows == 8 ? RowCfg<1>::kCtas : RowCfg<2>::kCtas), static_cast<int>(ceil_div(max_new * G, rows))};
+}
+
+template <int NT>
+int launch_rows(const KvAttn& a, const KvGrid& gr, float* parts, cudaStream_t stream) {
+  using C = RowCfg<NT>;
+  static PerDeviceOnce attr;
+  if (const int st = attr([&] {
+        return cudaFuncSetAttribute(kv_attn_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+               cudaSuccess;
+      }))
+    return st;
+  kv_attn_rows_kernel<NT><<<gr.ctas, kRowThreads, C::kSmem, stream>>>(a, gr.tiles, parts);
+  if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gr.ctas - 1, C::kRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<C::kRows>, a, gr.tiles, gr.ctas, static_cast<const float*>(parts)) ==
+                 cudaSuccess
+             ? HLWQ_OK
+             : HLWQ_ECUDA;
+}
+
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t Hq, int64_t H) {
+  const KvGrid gr = kv_grid(max_new, Hq / H);
+  return static_cast<size_t>(2) * gr.ctas * gr.rows * (kKvDim + 2) * sizeof(float);
+}
 
-int launch_kv_attention(const KvAttn& a, int64_t, void*, size_t, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(a.H), static_cast<unsigned>(ceil_div(a.G, kAtHeads)));
-  kv_attn_simple_kernel<<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? HLWQ_OK : HLWQ_ECUDA;
+int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
+  const KvGrid gr = kv_grid(max_new, a.G);
+  float* parts = static_cast<float*>(workspace);
+  return gr.rows == 8 ? launch_rows<1>(a, gr, parts, stream) : launch_rows<2>(a, gr, parts, stream);
 }
 
 }  // namespace hlwq
