@@ -301,7 +301,7 @@ extern "C" int hlwq_kv_paged_attention(const uint16_t* Q, int64_t ldq, int64_t T
       max_pages > INT32_MAX || !std::isfinite(scale))
     return HLWQ_EINVAL;
   if (const int st = kv_page_check(B, T, R, page_size)) return st;
-  if (kv_heads > 1024 || q_heads / kv_heads > 64) return HLWQ_EUNSUPPORTED;
+  if (kv_heads > 1024 || q_heads / kv_heads > 64 || T * q_heads > INT32_MAX) return HLWQ_EUNSUPPORTED;
   if (const int st = kv_pool_check(k_packed, k_norms, v_packed, v_norms, num_pages, k_window, v_window, R)) return st;
   if (!aligned16(Q) || !aligned16(out) || ldq % 8 || ldo % 8 || !aligned4(cu_new) || !aligned4(n_past) ||
       !aligned4(block_table) || !aligned4(codebook8))
@@ -438,7 +438,7 @@ extern "C" size_t hlwq_workspace_bytes(int op, int64_t a, int64_t b, int64_t c, 
   }
   if (op == HLWQ_OP_KV_ATTENTION) {
     if (E <= 0 || topk <= 0 || E % topk || E / topk > 64 || topk > 1024 || a > kKvMaxTokens ||
-        c > hlwq::kKvMaxRequests)
+        a * E > INT32_MAX || c > hlwq::kKvMaxRequests)
       return 0;
     return hlwq::kv_attention_workspace_bytes(a, std::min(a, b), c, E, topk);
   }

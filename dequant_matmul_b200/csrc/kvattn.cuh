@@ -42,71 +42,72 @@ struct KvAttn {
 //
 // An item is (request, row tile, kv head): a row tile is kRows consecutive
 // (token, query head) rows of a request, row = token * G + g.  An item's keys are
-// cut into units (64 encoded tokens, or kWinUnit window tokens); all items' units
+// cut into units (64 encoded tokens, or 64 window tokens); all items' units
 // in order, numbered 0 .. U - 1, are shared out evenly over the grid's CTAs in
 // contiguous ranges, whatever the requests' lengths are: one long request
 // is split over the machine, many short ones are not split.  Where a boundary
 // between two CTAs falls inside an item, its parts go to the workspace and
 // kv_attn_join_kernel adds them up.  Everything follows from cu and n_past, so every CTA
-// (and the join) works the shares out for itself: no plan is stored and the
-// host needs no lengths.
+// works its share out for itself: no plan is made beforehand and the host needs
+// no lengths.  A CTA that begins inside an item leaves a note for the join.
 
-constexpr int kUnit = 64;     // encoded tokens per unit
-constexpr int kWinUnit = 32;  // window tokens per unit (they are rotated here: about twice the work per token)
+constexpr int kUnit = 64;  // tokens per unit
 
 constexpr int64_t kMaxKeys = INT32_MAX - 4096;  // key positions are 32-bit below
 
 struct KvItem {
-  int b;            // request
-  int64_t c0, n;    // its first row of Q and its new tokens
-  int64_t p;        // cached tokens before the step
-  int64_t row0;     // first row of the tile, rows of the request in all: n * G
-  int64_t n_enc;    // encoded tokens of the request
-  int64_t e_lim;    // encoded tokens that the tile's last row sees
-  int64_t w_lim;    // tokens that it sees, window included
+  int b;         // request
+  int c0, n;     // its first row of Q and its new tokens
+  int p;         // cached tokens before the step
+  int row0;      // first row of the tile
+  int nrows;     // rows of the tile
+  int e_lim;     // encoded tokens that the tile's last row sees
+  int w_lim;     // tokens that it sees, window included
   int e_units, units;
 };
 
 // The pair (request, row tile) number `pair`; units = 0 where it has no rows.
+// (T * q_heads and key positions are below 2^31: checked by the host and here.)
 template <int kRows>
 __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, bool& bad) {
   KvItem it;
-  it.b = pair / tiles;
+  it.b = tiles == 1 ? pair : pair / tiles;
   const int rt = pair - it.b * tiles;
   it.c0 = __ldg(a.cu + it.b);
-  it.n = __ldg(a.cu + it.b + 1) - it.c0;
   it.p = __ldg(a.n_past + it.b);
-  it.row0 = static_cast<int64_t>(rt) * kRows;
-  it.units = 0;
-  it.e_units = 0;
-  if (it.c0 < 0 || it.n < 0 || it.c0 + it.n > a.T || it.p < 0 || it.p + it.n > kMaxKeys) {
+  const int64_t n = static_cast<int64_t>(__ldg(a.cu + it.b + 1)) - it.c0;
+  it.n = static_cast<int>(n);
+  it.units = it.e_units = 0;
+  if (it.c0 < 0 || n < 0 || it.c0 + n > a.T || it.p < 0 || it.p + n > kMaxKeys) {
     bad = true;
-    it.n = 0;
+    return it;
   }
-  const int64_t rows = it.n * a.G;
-  if (rt == 0 && rows > static_cast<int64_t>(tiles) * kRows) bad = true;  // more than max_new tokens
-  if (it.row0 >= rows) return it;
-  const int64_t last = (min(it.row0 + kRows, rows) - 1) / a.G;  // the tile's last token
-  const int64_t sees = it.p + last + 1;
-  it.n_enc = kv_enc(it.p + it.n, a.R);
-  it.e_lim = min(it.n_enc, sees);
+  const int rows = it.n * a.G;
+  if (rt == 0 && rows > tiles * kRows) bad = true;  // more than max_new tokens
+  it.row0 = rt * kRows;
+  it.nrows = min(kRows, rows - it.row0);
+  if (it.nrows <= 0) return it;
+  const int sees = it.p + (it.row0 + it.nrows - 1) / a.G + 1;  // keys of the tile's last token
+  it.e_lim = min(max(0, it.p + it.n - static_cast<int>(a.R)), sees);
   it.w_lim = sees;
-  it.e_units = static_cast<int>(ceil_div(it.e_lim, kUnit));
-  it.units = it.e_units + static_cast<int>(ceil_div(it.w_lim - it.e_lim, kWinUnit));
+  it.e_units = (it.e_lim + kUnit - 1) / kUnit;
+  it.units = it.e_units + (it.w_lim - it.e_lim + kUnit - 1) / kUnit;
   return it;
 }
 
-// The total of all units, and where `want` (0 <= want < U) lies: its pair and the
-// pair's first unit.  Called by all kThreads threads of the CTA with the same arguments.
+// The total of all units; `mine0` = the units before this thread's pairs.  Called
+// by all kThreads threads of the CTA.
 template <int kRows, int kThreads>
 __device__ __forceinline__ int64_t kv_total_units(const KvAttn& a, int tiles, int64_t* warp_sums, int64_t& mine0) {
   const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
   bool bad = false;
+#pragma unroll 1
   for (int i = 0; i < per; ++i) {
     const int pair = threadIdx.x * per + i;
-    if (pair < pairs) sum += static_cast<int64_t>(kv_item<kRows>(a, pair, tiles, bad).units) * a.H;
+    if (pair >= pairs) break;
+    sum += static_cast<int64_t>(kv_item<kRows>(a, pair, tiles, bad).units) * a.H;
   }
   if (bad && blockIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
   int64_t inc = sum;
@@ -135,6 +136,7 @@ __device__ __forceinline__ void kv_find_unit(const KvAttn& a, int tiles, int64_t
   int64_t u = mine0;
   bool bad = false;
   if (u <= want) {
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int pair = threadIdx.x * per + i;
       if (pair >= pairs) break;
@@ -149,6 +151,12 @@ __device__ __forceinline__ void kv_find_unit(const KvAttn& a, int tiles, int64_t
   }
   __syncthreads();
 }
+
+// What the CTA after a cut tells the join: the item whose first cut this is, and
+// how many CTAs' parts it has (0: no item is first cut here).
+struct KvCut {
+  int count, b, h, row0;
+};
 
 __device__ __forceinline__ int64_t kv_share(int64_t U, int c, int ctas) { return U * c / ctas; }
 
@@ -194,6 +202,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
@@ -242,14 +264,16 @@ __device__ __forceinline__ void cp_async_wait() {
 // are brought together with one select).  That is one table load and two integer
 // instructions for two values.
 //
-// P^T comes out of S^T's registers by two 8 x 8 transposes; row sums and maxima
+// P^T comes out of S^T's registers by two 8 x 8 transposes; row sums
 // stay in the lane until the end.  The running reference of a row's maximum is
 // raised only when a score exceeds it by 2^8 (exp2 stays below 2^8): the
 // sums are the same, most steps need no exchange between lanes.  A value's norm
 // rides on p; p n is kept in binary16's range by a power of two that follows the
 // largest norm (fv), so neither overflows and what is lost is 2^-39 of the
-// largest.  O^T's registers hold 32 consecutive dims of two rows: the final
-// rotation is five in-register and three shuffle stages.
+// largest.  O^T's registers hold 32 consecutive dims of two rows: the
+// rotation back is five in-register and three shuffle stages.  The window's keys
+// come after it and are multiplied as they are, un-rotated bf16 with the query's
+// own bits.
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
@@ -257,6 +281,7 @@ constexpr int kStage = 3136;  // 16 keys: K codes 1536, V codes 1536, K norms 32
 constexpr int kStages = 4;
 constexpr int kTabBytes = 64 * 128;
 constexpr float kMinM = -3.402823466e38f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NT>
 struct RowCfg {
@@ -265,7 +290,7 @@ struct RowCfg {
   static constexpr int kBuf = kStages * kStage;                  // per warp: ring, window tile, or 32 NT x 64 partial sums
   static constexpr int kMerge = NT * 32 * 32 * 8;                // bytes of a warp's O
   static constexpr int kWarpBytes = kBuf > kMerge ? kBuf : kMerge;
-  static constexpr int kSmem = 8192 /*align*/ + kTabBytes + kQFrag + kRowWarps * kWarpBytes;
+  static constexpr int kSmem = 8192 /*align*/ + kTabBytes + 2 * kQFrag + kRowWarps * kWarpBytes;
   static constexpr int kPart = kRows * (kKvDim + 2);             // floats of one partial result
   static constexpr int kCtas = NT == 1 ? 3 : 2;                  // resident per SM
 };
@@ -305,7 +330,7 @@ __device__ __forceinline__ void rows_pv(float (&o)[NT][16][4], const uint32_t (&
 
 template <int NT>
 __global__ void __launch_bounds__(kRowThreads, RowCfg<NT>::kCtas)
-kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
+kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut* __restrict__ cuts) {
   using C = RowCfg<NT>;
   extern __shared__ __align__(16) uint8_t rsm_raw[];
   __shared__ int64_t warp_sums[kRowWarps], found[2];
@@ -316,7 +341,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
   const uint32_t tab0 = (raw + 8191u) & ~8191u;  // 8 KB aligned: indices are or-ed in
   uint8_t* gtab = rsm_raw + (tab0 - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, l8 = lane & 7;
-  const uint32_t qfrag = tab0 + kTabBytes, wbuf = qfrag + C::kQFrag + warp * C::kWarpBytes;
+  const uint32_t qfrag = tab0 + kTabBytes, wbuf = qfrag + 2 * C::kQFrag + warp * C::kWarpBytes;
   uint8_t* gbuf = gtab + (wbuf - tab0);
   const uint32_t tab = tab0 + 4 * lane;
   const int page_size = static_cast<int>(a.P);
@@ -327,8 +352,10 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
 
   int64_t mine0;
   const int64_t U = kv_total_units<C::kRows, kRowThreads>(a, tiles, warp_sums, mine0);
-  const int64_t u0 = kv_share(U, blockIdx.x, gridDim.x), u1 = kv_share(U, blockIdx.x + 1, gridDim.x);
-  if (u0 >= u1) return;
+  if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
+  const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));  // every one of these has work
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const int64_t u0 = kv_share(U, blockIdx.x, ctas), u1 = kv_share(U, blockIdx.x + 1, ctas);
   kv_find_unit<C::kRows, kRowThreads>(a, tiles, mine0, u0, found);
   int pair = static_cast<int>(found[0]);
   int64_t at = found[1];  // first unit of the pair
@@ -344,22 +371,40 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
     const int ta = static_cast<int>(u - at - static_cast<int64_t>(h) * it.units);
     const int tb = static_cast<int>(min(static_cast<int64_t>(it.units), ta + (u1 - u)));
     u += tb - ta;
-    const int nrows = static_cast<int>(min(static_cast<int64_t>(C::kRows), it.n * a.G - it.row0));
+    const int nrows = it.nrows;
+    if (threadIdx.x == 0 && ta > 0 && u == u0 + (tb - ta)) {
+      // this CTA begins inside an item: is the boundary before it the item's first cut?
+      const int64_t s0 = at + static_cast<int64_t>(h) * it.units;
+      int count = 0;
+      if (kv_share(U, blockIdx.x - 1, ctas) <= s0) {
+        // parts: the CTA before this one, this one, and those that begin before the item's end
+        const int64_t s1 = s0 + it.units;
+        count = 1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - blockIdx.x;
+      }
+      cuts[blockIdx.x] = {count, it.b, h, it.row0};
+    }
 
     // rotate the tile's rows into matrix-instruction order
     for (int r0 = warp * 4; r0 < C::kRows; r0 += kRowWarps * 4) {
       const int r = r0 + (lane >> 3);
       const bool on = r < nrows;
-      const int64_t row = it.row0 + (on ? r : 0), tok = row / a.G;
+      const int row = it.row0 + (on ? r : 0), tok = row / a.G;
       float v[32];
       load_bf16x32(v, a.q + (it.c0 + tok) * a.ldq + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * l8, on);
+      const uint32_t dst = qfrag + ((r >> 3) * 16 * 32 + (r & 7) * 4 + (l8 >> 1)) * 8 + (l8 & 1) * 8 * 256;
+      // as it is (for the window's keys), its bf16 bits exact
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + C::kQFrag + s * 256),
+                     "r"(__byte_perm(__float_as_uint(v[4 * s]), __float_as_uint(v[4 * s + 1]), 0x7632)),
+                     "r"(__byte_perm(__float_as_uint(v[4 * s + 2]), __float_as_uint(v[4 * s + 3]), 0x7632))
+                     : "memory");
       kv_fwht(v, lane);
       float mx = 0.0f, inv;
 #pragma unroll
       for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
       const float sc = pow2_scale(oct_max(mx), inv);
-      if (l8 == 0) qmul[r] = inv * a.scale * (1.4426950408889634f / 256.0f);
-      const uint32_t dst = qfrag + ((r >> 3) * 16 * 32 + (r & 7) * 4 + (l8 >> 1)) * 8 + (l8 & 1) * 8 * 256;
+      if (l8 == 0) qmul[r] = inv * a.scale * (kLog2e / 256.0f);
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + s * 256),
@@ -380,23 +425,22 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
         m[nt][k] = kMinM;
         l[nt][k] = 0.0f;
         qm[nt][k] = qmul[r];
-        lim[nt][k] = r < nrows ? static_cast<int>(it.p + (it.row0 + r) / a.G + 1) : 0;
+        lim[nt][k] = r < nrows ? it.p + (it.row0 + r) / a.G + 1 : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[nt][i][k] = o[nt][i][2 + k] = 0.0f;
       }
 
-    // scores of 16 keys (d, per row tile) -> the operand of P V
-    auto softmax = [&](float (&d)[NT][4], float nk0, float nk1, float nv0, float nv1, int key, int end,
-                       uint32_t(&b)[NT][2]) {
-      // key: index of this lane's first key; the second one is 8 further; keys from `end` on are not there
+    // scores of 16 keys, times their factors k0 (this lane's first key, index `key`) and
+    // k1 (8 further); keys from `end` on are not there; the rows' references follow
+    auto score = [&](float (&d)[NT][4], float k0, float k1, int key, int end) {
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int see = min(lim[nt][k], end);
-          d[nt][k] = key < see ? d[nt][k] * (nk0 * qm[nt][k]) : -INFINITY;
-          d[nt][2 + k] = key + 8 < see ? d[nt][2 + k] * (nk1 * qm[nt][k]) : -INFINITY;
+          d[nt][k] = key < see ? d[nt][k] * (k0 * qm[nt][k]) : -INFINITY;
+          d[nt][2 + k] = key + 8 < see ? d[nt][2 + k] * (k1 * qm[nt][k]) : -INFINITY;
           over |= fmaxf(d[nt][k], d[nt][2 + k]) > m[nt][k] + 8.0f;
         }
       if (__any_sync(0xffffffffu, over)) {
@@ -418,37 +462,19 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
             }
           }
       }
-      if (__any_sync(0xffffffffu, fmaxf(nv0, nv1) * fv > 128.0f)) {
-        float x = fmaxf(nv0, nv1);
-#pragma unroll
-        for (int s = 4; s < 32; s <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
-        const int e = min(144, static_cast<int>(__float_as_uint(x) >> 23) + 1);  // x < 2^(e - 127)
-        const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23), f = nf / fv;  // x nf in [16, 32)
-        fv = nf;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
-      }
-      const float f0 = nv0 * fv, f1 = nv1 * fv;
+      // p = exp2(s - reference), up to 2^8, and the row sums
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = exp2f(d[nt][k] - m[nt][k & 1]);
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
-        // a key that is masked out has no say, whatever its norm is
-        b[nt][0] = transpose_8x8(pack_half2(p[0] > 0.0f || p[0] != p[0] ? p[0] * f0 : 0.0f, p[1] > 0.0f || p[1] != p[1] ? p[1] * f0 : 0.0f));
-        b[nt][1] = transpose_8x8(pack_half2(p[2] > 0.0f || p[2] != p[2] ? p[2] * f1 : 0.0f, p[3] > 0.0f || p[3] != p[3] ? p[3] * f1 : 0.0f));
+        for (int k = 0; k < 4; ++k) d[nt][k] = exp2f(d[nt][k] - m[nt][k & 1]);
+        l[nt][0] += d[nt][0] + d[nt][2];
+        l[nt][1] += d[nt][1] + d[nt][3];
       }
     };
 
     // ---- encoded keys: tiles of 16, one warp each, kStages - 1 of them under way
     const int e_tb = min(tb, it.e_units);
-    const int k_end = static_cast<int>(min(static_cast<int64_t>(e_tb) * kUnit, it.e_lim));
+    const int k_end = min(e_tb * kUnit, it.e_lim);
     const int k_first = ta * kUnit + 16 * warp;
     auto request = [&](int k0, int stage) {  // false: the page is not there
       bool there = false;
@@ -525,10 +551,34 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) d[0][nt][k] += d[1][nt][k];
           uint32_t b[NT][2];
-          softmax(d[0], half_bits_to_float(static_cast<uint16_t>(nkw >> ns16)),
-                  half_bits_to_float(static_cast<uint16_t>(nkw2 >> ns16)),
-                  half_bits_to_float(static_cast<uint16_t>(nvw >> ns16)),
-                  half_bits_to_float(static_cast<uint16_t>(nvw2 >> ns16)), k0 + g, k_end, b);
+          score(d[0], half_bits_to_float(static_cast<uint16_t>(nkw >> ns16)),
+                half_bits_to_float(static_cast<uint16_t>(nkw2 >> ns16)), k0 + g, k_end);
+          const float nv0 = half_bits_to_float(static_cast<uint16_t>(nvw >> ns16));
+          const float nv1 = half_bits_to_float(static_cast<uint16_t>(nvw2 >> ns16));
+          if (__any_sync(0xffffffffu, (k0 + g < k_end && nv0 * fv > 128.0f) || (k0 + g + 8 < k_end && nv1 * fv > 128.0f))) {
+            float x = fmaxf(k0 + g < k_end ? nv0 : 0.0f, k0 + g + 8 < k_end ? nv1 : 0.0f);
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
+            const int e = min(144, static_cast<int>(__float_as_uint(x) >> 23) + 1);  // x < 2^(e - 127)
+            const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23), f = nf / fv;  // x nf in [16, 32)
+            fv = nf;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
+          }
+          const float f0 = nv0 * fv, f1 = nv1 * fv;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            // a key that is masked out has no say, whatever its norm is (NaN stays NaN)
+            float p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = d[0][nt][k] == 0.0f ? 0.0f : d[0][nt][k] * (k < 2 ? f0 : f1);
+            b[nt][0] = transpose_8x8(pack_half2(p[0], p[1]));
+            b[nt][1] = transpose_8x8(pack_half2(p[2], p[3]));
+          }
           uint32_t vw[4][3];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -543,62 +593,99 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
       __syncwarp();
     }
 
-    // ---- window keys, 16 at a time: rotated by eight lanes per vector into the
-    // warp's buffer as binary16 with a power-of-two scale in the norm's place
-    const int w_first = static_cast<int>(it.e_lim) + (max(ta, it.e_units) - it.e_units) * kWinUnit;
-    const int w_end = min(static_cast<int>(it.e_lim) + (tb - it.e_units) * kWinUnit, static_cast<int>(it.w_lim));
-    for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {
-      float nrm[2][2];  // [K, V][keys g, g + 8]
-      float d[NT][4];
-      uint32_t b[NT][2];
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
-        __syncwarp();
-        float* scales = reinterpret_cast<float*>(gbuf + 16 * 520);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int key = 4 * i + (lane >> 3);
-          const bool on = k0 + key < w_end;
+    // ---- out of the rotated domain: O^T <- H O^T / (256 fv), in registers
+    if (ta < e_tb) {
+      const float f = 1.0f / (256.0f * fv);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
           float v[32];
-          load_bf16x32(v, (kv ? a.vwin : a.kwin) + ((static_cast<int64_t>(it.b) * a.H + h) * a.R + (on ? (k0 + key) % static_cast<int>(a.R) : 0)) * kKvDim + 32 * l8, on);
-          kv_fwht(v, lane);
-          float mx = 0.0f, inv;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
-          const float sc = pow2_scale(oct_max(mx), inv);
-          if (l8 == 0) scales[key] = inv;
+          for (int i = 0; i < 16; ++i) v[2 * i] = o[nt][i][k] * f, v[2 * i + 1] = o[nt][i][2 + k] * f;
+          kv_stage<float, 1>(v);
+          kv_stage<float, 2>(v);
+          kv_stage<float, 4>(v);
+          kv_stage<float, 8>(v);
+          kv_stage<float, 16>(v);
+          kv_stage_x<float, 4>(v, lane);
+          kv_stage_x<float, 8>(v, lane);
+          kv_stage_x<float, 16>(v, lane);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint2*>(gbuf + key * 520 + 64 * l8 + 8 * e) =
-                make_uint2(pack_half2(v[4 * e] * sc, v[4 * e + 1] * sc), pack_half2(v[4 * e + 2] * sc, v[4 * e + 3] * sc));
+          for (int i = 0; i < 16; ++i) o[nt][i][k] = v[2 * i], o[nt][i][2 + k] = v[2 * i + 1];
         }
-        __syncwarp();
-        nrm[kv][0] = scales[g];
-        nrm[kv][1] = scales[g + 8];
-        if (kv == 0) {
+    }
+
+    // ---- window keys, 16 at a time and as they are: bf16 operands, scores exact to
+    // fp32, p in two bf16 parts (16 bits)
+    const int w_first = it.e_lim + (max(ta, it.e_units) - it.e_units) * kUnit;
+    const int w_end = min(it.e_lim + (tb - it.e_units) * kUnit, it.w_lim);
+    if (w_first < w_end) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) qm[nt][0] = qm[nt][1] = a.scale * kLog2e;
+    }
+#pragma unroll 1
+    for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {
+      const int R = static_cast<int>(a.R);
+      const int64_t ring = (static_cast<int64_t>(it.b) * a.H + h) * R;
+      float d[NT][4];
 #pragma unroll
-          for (int s = 0; s < 16; ++s) {
-            const uint2 x = lds64(wbuf + g * 520 + 128 * t4 + 8 * s), y = lds64(wbuf + (g + 8) * 520 + 128 * t4 + 8 * s);
+      for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
+      {
+        const bool on0 = k0 + g < w_end, on1 = k0 + g + 8 < w_end;
+        const uint16_t* s0 = a.kwin + (ring + (on0 ? (k0 + g) % R : 0)) * kKvDim + 64 * t4;
+        const uint16_t* s1 = a.kwin + (ring + (on1 ? (k0 + g + 8) % R : 0)) * kKvDim + 64 * t4;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q = lds64(qfrag + ((nt * 16 + s) * 32 + lane) * 8);
-              mma_16816(d[nt], x.x, y.x, x.y, y.y, q.x, q.y);
-            }
+        for (int s = 0; s < 8; ++s) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+          if (on0) x = __ldg(reinterpret_cast<const uint4*>(s0) + s);
+          if (on1) y = __ldg(reinterpret_cast<const uint4*>(s1) + s);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 q0 = lds64(qfrag + C::kQFrag + ((nt * 16 + 2 * s) * 32 + lane) * 8);
+            const uint2 q1 = lds64(qfrag + C::kQFrag + ((nt * 16 + 2 * s + 1) * 32 + lane) * 8);
+            mma_16816_bf16(d[nt], x.x, y.x, x.y, y.y, q0.x, q0.y);
+            mma_16816_bf16(d[nt], x.z, y.z, x.w, y.w, q1.x, q1.y);
           }
         }
       }
-      softmax(d, nrm[0][0], nrm[0][1], nrm[1][0], nrm[1][1], k0 + g, w_end, b);
+      score(d, 1.0f, 1.0f, k0 + g, w_end);
+      uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t x[4];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = lds32(wbuf + (2 * t4 + (k & 1) + 8 * (k >> 1)) * 520 + 64 * g + 4 * i);
-        const uint32_t a0 = __byte_perm(x[0], x[1], 0x5410), a1 = __byte_perm(x[0], x[1], 0x7632);
-        const uint32_t a2 = __byte_perm(x[2], x[3], 0x5410), a3 = __byte_perm(x[2], x[3], 0x7632);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t hi = pack_bf162(d[nt][2 * k], d[nt][2 * k + 1]);
+          bh[nt][k] = transpose_8x8(hi);
+          bl[nt][k] = transpose_8x8(pack_bf162(d[nt][2 * k] - bf16x2_lo(hi), d[nt][2 * k + 1] - bf16x2_hi(hi)));
+        }
+      const uint16_t* sv[4];
+      bool on[4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+      for (int k = 0; k < 4; ++k) {
+        const int key = k0 + 2 * t4 + (k & 1) + 8 * (k >> 1);
+        on[k] = key < w_end;
+        sv[k] = a.vwin + (ring + (on[k] ? key % R : 0)) * kKvDim + 32 * g;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (on[k]) u = __ldg(reinterpret_cast<const uint4*>(sv[k]) + c);
+          x[k][0] = u.x, x[k][1] = u.y, x[k][2] = u.z, x[k][3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410), a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
+          const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410), a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816_bf16(o[nt][4 * c + i], a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
+            mma_16816_bf16(o[nt][4 * c + i], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+          }
+        }
       }
     }
 
@@ -624,7 +711,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
         float x = mstat[0][r];
 #pragma unroll
         for (int w = 1; w < kRowWarps; ++w) x = fmaxf(x, mstat[w][r]);
-        const float f = exp2f(m[nt][k] - x) / fv;
+        const float f = exp2f(m[nt][k] - x);
         // [row tile][row parity][tile m, dim parity][lane]
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -642,7 +729,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
       for (int i = 0; i < 32; ++i) v[i] = 0.0f;
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) {
-        const float* src = reinterpret_cast<const float*>(gtab + (qfrag + C::kQFrag - tab0) + w * C::kWarpBytes) + warp * 1024 + lane;
+        const float* src = reinterpret_cast<const float*>(gtab + (qfrag + 2 * C::kQFrag - tab0) + w * C::kWarpBytes) + warp * 1024 + lane;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] += src[32 * i];
       }
@@ -652,17 +739,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) sum += lstat[w][r] * exp2f(mstat[w][r] - mx);
       if (ta == 0 && tb == it.units) {
-        kv_stage<float, 1>(v);
-        kv_stage<float, 2>(v);
-        kv_stage<float, 4>(v);
-        kv_stage<float, 8>(v);
-        kv_stage<float, 16>(v);
-        kv_stage_x<float, 4>(v, lane);
-        kv_stage_x<float, 8>(v, lane);
-        kv_stage_x<float, 16>(v, lane);
         if (r < nrows) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / (256.0f * sum);
-          const int64_t row = it.row0 + r, tok = row / a.G;
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const int row = it.row0 + r, tok = row / a.G;
           uint4* dst = reinterpret_cast<uint4*>(a.out + (it.c0 + tok) * a.ldo + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * g);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -689,41 +768,28 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts) {
   }
 }
 
-// Adds the parts of the items that a boundary between CTAs cut: CTA (c, row)
-// joins that row of the item in which boundary c (before CTA c of the attention
-// grid of `ctas`) is the first one.  Eight warps take the parts in turn, each
-// lane eight dims; then one warp rotates and writes the row.
+// Adds the parts of the items that boundaries between CTAs cut.  CTA (c, r)
+// takes row r of the item that attention CTA c + 1 noted as first cut at its
+// beginning: part 0 is CTA c's last one, part j > 0 CTA c + j's first one.
+// Eight warps take the parts in turn, each lane eight dims.
 constexpr int kJoinThreads = 256;
 template <int kRows>
 __global__ void __launch_bounds__(kJoinThreads)
-kv_attn_join_kernel(const KvAttn a, int tiles, int ctas, const float* __restrict__ parts) {
-  __shared__ int64_t warp_sums[kJoinThreads / 32], found[2];
+kv_attn_join_kernel(const KvAttn a, const float* __restrict__ parts, const KvCut* __restrict__ cuts) {
   __shared__ float acc[kJoinThreads / 32][kKvDim], ms[kJoinThreads / 32], ls[kJoinThreads / 32];
   constexpr int kPart = kRows * (kKvDim + 2);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, c = blockIdx.x + 1;
-  int64_t mine0;
-  const int64_t U = kv_total_units<kRows, kJoinThreads>(a, tiles, warp_sums, mine0);
-  const int64_t uc = kv_share(U, c, ctas), ub = kv_share(U, c - 1, ctas);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, c = blockIdx.x;
   pdl_wait();  // in every CTA: the join has not ended before the attention has
-  if (uc >= U || uc == ub) return;
-  kv_find_unit<kRows, kJoinThreads>(a, tiles, mine0, uc, found);
-  bool bad = false;
-  const KvItem it = kv_item<kRows>(a, static_cast<int>(found[0]), tiles, bad);
-  const int h = static_cast<int>((uc - found[1]) / it.units);
-  const int64_t s0 = found[1] + static_cast<int64_t>(h) * it.units, s1 = s0 + it.units;
-  if (uc == s0 || ub > s0) return;  // no cut, or not its first
-  if (it.row0 + r >= it.n * a.G) return;
+  const KvCut cut = cuts[c + 1];
+  if (cut.count == 0) return;
+  const int c0 = __ldg(a.cu + cut.b), row = cut.row0 + r;
+  if (row >= (__ldg(a.cu + cut.b + 1) - c0) * a.G) return;
   float v[8];
   float m = kMinM, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  // part 0 is CTA c - 1's, part j >= 1 CTA c + j - 1's
-  int count = 1;
-  for (int k = c; k < ctas && kv_share(U, k, ctas) < s1; ++k) ++count;
-  for (int j = warp; j < count; j += kJoinThreads / 32) {
-    const int k = c - 1 + j;
-    if (kv_share(U, k, ctas) == kv_share(U, k + 1, ctas)) continue;
-    const float* part = parts + static_cast<int64_t>(2 * k + (j == 0 ? 1 : 0)) * kPart;
+  for (int j = warp; j < cut.count; j += kJoinThreads / 32) {
+    const float* part = parts + static_cast<int64_t>(2 * (c + j) + (j == 0 ? 1 : 0)) * kPart;
     const float pm = part[kRows * kKvDim + r], pl = part[kRows * (kKvDim + 1) + r];
     const float4 x = reinterpret_cast<const float4*>(part + r * kKvDim)[2 * lane];
     const float4 y = reinterpret_cast<const float4*>(part + r * kKvDim)[2 * lane + 1];
@@ -739,37 +805,22 @@ kv_attn_join_kernel(const KvAttn a, int tiles, int ctas, const float* __restrict
   if (lane == 0) ms[warp] = m, ls[warp] = l;
   __syncthreads();
   if (warp) return;
-  for (int w = 1; w < kJoinThreads / 32; ++w) {
+  const int warps = min(kJoinThreads / 32, cut.count);
+  for (int w = 1; w < warps; ++w) {
     const float nm = fmaxf(m, ms[w]), fo = exp2f(m - nm), fn = exp2f(ms[w] - nm);
     m = nm;
     l = l * fo + ls[w] * fn;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] * fo + acc[w][8 * lane + i] * fn;
   }
-#pragma unroll
-  for (int s = 1; s < 8; s <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((i & s) == 0) {
-        const float x = v[i], y = v[i + s];
-        v[i] = x + y;
-        v[i + s] = x - y;
-      }
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = __shfl_xor_sync(0xffffffffu, v[i], s);
-      v[i] = (lane & s) ? x - v[i] : v[i] + x;
-    }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / (256.0f * l);
-  const int64_t row = it.row0 + r, tok = row / a.G;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int tok = row / a.G;
   uint4 x;
   x.x = float_to_bf16_bits(v[0] * inv) | (float_to_bf16_bits(v[1] * inv) << 16);
   x.y = float_to_bf16_bits(v[2] * inv) | (float_to_bf16_bits(v[3] * inv) << 16);
   x.z = float_to_bf16_bits(v[4] * inv) | (float_to_bf16_bits(v[5] * inv) << 16);
   x.w = float_to_bf16_bits(v[6] * inv) | (float_to_bf16_bits(v[7] * inv) << 16);
-  reinterpret_cast<uint4*>(a.out + (it.c0 + tok) * a.ldo + (h * a.G + (row - tok * a.G)) * kKvDim)[lane] = x;
+  reinterpret_cast<uint4*>(a.out + (c0 + tok) * a.ldo + (cut.h * a.G + (row - tok * a.G)) * kKvDim)[lane] = x;
 }
 
 // The attention grid and its row tiles for max_new new tokens of a request.
@@ -782,7 +833,7 @@ inline KvGrid kv_grid(int64_t max_new, int64_t G) {
 }
 
 template <int NT>
-int launch_rows(const KvAttn& a, const KvGrid& gr, float* parts, cudaStream_t stream) {
+int launch_rows(const KvAttn& a, const KvGrid& gr, void* workspace, cudaStream_t stream) {
   using C = RowCfg<NT>;
   static PerDeviceOnce attr;
   if (const int st = attr([&] {
@@ -790,7 +841,9 @@ int launch_rows(const KvAttn& a, const KvGrid& gr, float* parts, cudaStream_t st
                cudaSuccess;
       }))
     return st;
-  kv_attn_rows_kernel<NT><<<gr.ctas, kRowThreads, C::kSmem, stream>>>(a, gr.tiles, parts);
+  float* parts = static_cast<float*>(workspace);
+  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.ctas * C::kPart);
+  kv_attn_rows_kernel<NT><<<gr.ctas, kRowThreads, C::kSmem, stream>>>(a, gr.tiles, parts, cuts);
   if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(gr.ctas - 1, C::kRows);
@@ -801,8 +854,8 @@ int launch_rows(const KvAttn& a, const KvGrid& gr, float* parts, cudaStream_t st
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<C::kRows>, a, gr.tiles, gr.ctas, static_cast<const float*>(parts)) ==
-                 cudaSuccess
+  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<C::kRows>, a, static_cast<const float*>(parts),
+                            static_cast<const KvCut*>(cuts)) == cudaSuccess
              ? HLWQ_OK
              : HLWQ_ECUDA;
 }
@@ -811,13 +864,12 @@ int launch_rows(const KvAttn& a, const KvGrid& gr, float* parts, cudaStream_t st
 
 size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t Hq, int64_t H) {
   const KvGrid gr = kv_grid(max_new, Hq / H);
-  return static_cast<size_t>(2) * gr.ctas * gr.rows * (kKvDim + 2) * sizeof(float);
+  return static_cast<size_t>(gr.ctas) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
 }
 
 int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
   const KvGrid gr = kv_grid(max_new, a.G);
-  float* parts = static_cast<float*>(workspace);
-  return gr.rows == 8 ? launch_rows<1>(a, gr, parts, stream) : launch_rows<2>(a, gr, parts, stream);
+  return gr.rows == 8 ? launch_rows<1>(a, gr, workspace, stream) : launch_rows<2>(a, gr, workspace, stream);
 }
 
 }  // namespace hlwq
