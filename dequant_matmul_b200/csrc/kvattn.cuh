@@ -390,7 +390,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       const bool on = r < nrows;
       const int row = it.row0 + (on ? r : 0), tok = row / a.G;
       float v[32];
-      load_bf16x32(v, a.q + (it.c0 + tok) * a.ldq + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * l8, on);
+      load_bf16x32(v, a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * l8, on);
       const uint32_t dst = qfrag + ((r >> 3) * 16 * 32 + (r & 7) * 4 + (l8 >> 1)) * 8 + (l8 & 1) * 8 * 256;
       // as it is (for the window's keys), its bf16 bits exact
 #pragma unroll
@@ -742,7 +742,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         if (r < nrows) {
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
           const int row = it.row0 + r, tok = row / a.G;
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (it.c0 + tok) * a.ldo + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * g);
+          uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(it.c0 + tok) * a.ldo + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * g);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint4 x;
@@ -768,50 +768,64 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   }
 }
 
-// Adds the parts of the items that boundaries between CTAs cut.  CTA (c, r)
-// takes row r of the item that attention CTA c + 1 noted as first cut at its
+// Adds the parts of the items that boundaries between CTAs cut.  CTA (c, y)
+// takes rows of the item that attention CTA c + 1 noted as first cut at its
 // beginning: part 0 is CTA c's last one, part j > 0 CTA c + j's first one.
-// Eight warps take the parts in turn, each lane eight dims.
+// Few-row tiles have many parts: one row per CTA, eight warps take its parts in
+// turn.  128-row tiles have few: a warp per row.  A lane holds eight dims.
 constexpr int kJoinThreads = 256;
+template <int kRows>
+struct JoinCfg {
+  static constexpr int kSplit = kRows == 128 ? 1 : 8;              // warps per row
+  static constexpr int kPerCta = kJoinThreads / 32 / kSplit;       // rows per CTA
+  static constexpr int kPart = kRows * (kKvDim + 2);
+  // float4 c of row r: row after row, or (128 rows) column after column
+  static __device__ __forceinline__ int at(int r, int c) { return kRows == 128 ? c * kRows + r : r * (kKvDim / 4) + c; }
+};
+
 template <int kRows>
 __global__ void __launch_bounds__(kJoinThreads)
 kv_attn_join_kernel(const KvAttn a, const float* __restrict__ parts, const KvCut* __restrict__ cuts) {
-  __shared__ float acc[kJoinThreads / 32][kKvDim], ms[kJoinThreads / 32], ls[kJoinThreads / 32];
-  constexpr int kPart = kRows * (kKvDim + 2);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y, c = blockIdx.x;
+  using J = JoinCfg<kRows>;
+  __shared__ float acc[J::kSplit][kKvDim], ms[J::kSplit], ls[J::kSplit];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+  const int r = blockIdx.y * J::kPerCta + (J::kSplit == 1 ? warp : 0), first = J::kSplit == 1 ? 0 : warp;
   pdl_wait();  // in every CTA: the join has not ended before the attention has
   const KvCut cut = cuts[c + 1];
   if (cut.count == 0) return;
   const int c0 = __ldg(a.cu + cut.b), row = cut.row0 + r;
-  if (row >= (__ldg(a.cu + cut.b + 1) - c0) * a.G) return;
+  if (row >= (__ldg(a.cu + cut.b + 1) - c0) * a.G) return;  // the same for all warps of a row
   float v[8];
   float m = kMinM, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  for (int j = warp; j < cut.count; j += kJoinThreads / 32) {
-    const float* part = parts + static_cast<int64_t>(2 * (c + j) + (j == 0 ? 1 : 0)) * kPart;
-    const float pm = part[kRows * kKvDim + r], pl = part[kRows * (kKvDim + 1) + r];
-    const float4 x = reinterpret_cast<const float4*>(part + r * kKvDim)[2 * lane];
-    const float4 y = reinterpret_cast<const float4*>(part + r * kKvDim)[2 * lane + 1];
+  auto add = [&](float pm, float pl, const float (&x)[8]) {
     const float nm = fmaxf(m, pm), fo = exp2f(m - nm), fn = exp2f(pm - nm);
     m = nm;
     l = l * fo + pl * fn;
-    const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * fo + w[i] * fn;
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * fo + x[i] * fn;
+  };
+#pragma unroll 4
+  for (int j = first; j < cut.count; j += J::kSplit) {
+    const float* part = parts + static_cast<int64_t>(2 * (c + j) + (j == 0 ? 1 : 0)) * J::kPart;
+    const float4 x = reinterpret_cast<const float4*>(part)[J::at(r, 2 * lane)];
+    const float4 y = reinterpret_cast<const float4*>(part)[J::at(r, 2 * lane + 1)];
+    add(part[kRows * kKvDim + r], part[kRows * (kKvDim + 1) + r], {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w});
   }
+  if constexpr (J::kSplit > 1) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[warp][8 * lane + i] = v[i];
-  if (lane == 0) ms[warp] = m, ls[warp] = l;
-  __syncthreads();
-  if (warp) return;
-  const int warps = min(kJoinThreads / 32, cut.count);
-  for (int w = 1; w < warps; ++w) {
-    const float nm = fmaxf(m, ms[w]), fo = exp2f(m - nm), fn = exp2f(ms[w] - nm);
-    m = nm;
-    l = l * fo + ls[w] * fn;
+    for (int i = 0; i < 8; ++i) acc[warp][8 * lane + i] = v[i];
+    if (lane == 0) ms[warp] = m, ls[warp] = l;
+    __syncthreads();
+    if (warp) return;
+    const int warps = min(J::kSplit, cut.count);
+    for (int w = 1; w < warps; ++w) {
+      float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * fo + acc[w][8 * lane + i] * fn;
+      for (int i = 0; i < 8; ++i) x[i] = acc[w][8 * lane + i];
+      add(ms[w], ls[w], x);
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int tok = row / a.G;
@@ -820,33 +834,14 @@ kv_attn_join_kernel(const KvAttn a, const float* __restrict__ parts, const KvCut
   x.y = float_to_bf16_bits(v[2] * inv) | (float_to_bf16_bits(v[3] * inv) << 16);
   x.z = float_to_bf16_bits(v[4] * inv) | (float_to_bf16_bits(v[5] * inv) << 16);
   x.w = float_to_bf16_bits(v[6] * inv) | (float_to_bf16_bits(v[7] * inv) << 16);
-  reinterpret_cast<uint4*>(a.out + (c0 + tok) * a.ldo + (cut.h * a.G + (row - tok * a.G)) * kKvDim)[lane] = x;
+  reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(c0 + tok) * a.ldo + (cut.h * a.G + (row - tok * a.G)) * kKvDim)[lane] = x;
 }
 
-// The attention grid and its row tiles for max_new new tokens of a request.
-struct KvGrid {
-  int rows, ctas, tiles;
-};
-inline KvGrid kv_grid(int64_t max_new, int64_t G) {
-  const int rows = max_new * G <= 8 ? 8 : 16;
-  return {rows, sm_count() * (rows == 8 ? RowCfg<1>::kCtas : RowCfg<2>::kCtas), static_cast<int>(ceil_div(max_new * G, rows))};
-}
-
-template <int NT>
-int launch_rows(const KvAttn& a, const KvGrid& gr, void* workspace, cudaStream_t stream) {
-  using C = RowCfg<NT>;
-  static PerDeviceOnce attr;
-  if (const int st = attr([&] {
-        return cudaFuncSetAttribute(kv_attn_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
-               cudaSuccess;
-      }))
-    return st;
-  float* parts = static_cast<float*>(workspace);
-  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.ctas * C::kPart);
-  kv_attn_rows_kernel<NT><<<gr.ctas, kRowThreads, C::kSmem, stream>>>(a, gr.tiles, parts, cuts);
-  if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
+template <int kRows>
+int launch_join(const KvAttn& a, int ctas, const float* parts, const KvCut* cuts, cudaStream_t stream) {
+  if (ctas < 2) return HLWQ_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(gr.ctas - 1, C::kRows);
+  cfg.gridDim = dim3(ctas - 1, kRows / JoinCfg<kRows>::kPerCta);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute pdl;
@@ -854,22 +849,23 @@ int launch_rows(const KvAttn& a, const KvGrid& gr, void* workspace, cudaStream_t
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<C::kRows>, a, static_cast<const float*>(parts),
-                            static_cast<const KvCut*>(cuts)) == cudaSuccess
-             ? HLWQ_OK
-             : HLWQ_ECUDA;
+  return cudaLaunchKernelEx(&cfg, kv_attn_join_kernel<kRows>, a, parts, cuts) == cudaSuccess ? HLWQ_OK : HLWQ_ECUDA;
+}
+
+template <int NT>
+int launch_rows(const KvAttn& a, int ctas, int tiles, float* parts, KvCut* cuts, cudaStream_t stream) {
+  using C = RowCfg<NT>;
+  static PerDeviceOnce attr;
+  if (const int st = attr([&] {
+        return cudaFuncSetAttribute(kv_attn_rows_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) ==
+               cudaSuccess;
+      }))
+    return st;
+  kv_attn_rows_kernel<NT><<<ctas, kRowThreads, C::kSmem, stream>>>(a, tiles, parts, cuts);
+  if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
+  return launch_join<C::kRows>(a, ctas, parts, cuts, stream);
 }
 
 }  // namespace
-
-size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t Hq, int64_t H) {
-  const KvGrid gr = kv_grid(max_new, Hq / H);
-  return static_cast<size_t>(gr.ctas) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
-}
-
-int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
-  const KvGrid gr = kv_grid(max_new, a.G);
-  return gr.rows == 8 ? launch_rows<1>(a, gr, workspace, stream) : launch_rows<2>(a, gr, workspace, stream);
-}
 
 }  // namespace hlwq

@@ -1,0 +1,834 @@
+#pragma once
+// Attention over the paged Q3 KV cache for many rows per kv head (chunks of new
+// tokens): 128 (token, head) rows x 64 keys at a time on the tcgen05 tensor
+// cores (sm_100a).  The mathematics, the sharing of the work and the join are
+// those of kvattn.cuh.
+//
+// A CTA works on one row tile at a time.  Tensor memory: O [128 x 256] fp32 in
+// columns 0..255, the rotated rows Q [128 x 256] binary16 in 256..383, two score
+// tiles S [128 x 64] fp32 in 384..511, each overwritten by its P (binary16, 32
+// columns).  Q and P are the A operands (so shared memory carries only what is
+// decoded); K [64 keys][256 dims] and V^T [256 dims][64 keys] are the B operands,
+// both K-major with the 128-byte swizzle, decoded there from the 3-bit codes.
+//
+// Roles (14 warps):
+//   0..3   softmax: thread = row.  Puts Q into tensor memory (rotated per thread,
+//          in two passes over the columns of O, which are free then), turns S(j)
+//          into P(j), rescales O when a row's reference rises (seldom, as in the
+//          few-row kernel), rotates O back, writes the rows.
+//   4..11  decode: code pairs -> binary16 pairs through the 64-entry table (one
+//          copy per lane) -> 16-byte stores into the K and V^T tiles; window
+//          tiles are copied (K) and transposed (V) as they are, bf16.
+//   12     issues the MMAs: S(j + 1), then O += P(j) V(j).
+//   13     fetches codes and norms, 16 keys (never two pages) per bulk copy.
+//
+// Keys stand in the tiles in an order that keeps every shared-memory access of
+// the decoders free of bank conflicts: row n = 8 w + g of the K tile is key
+// 16 (g & 3) + 2 (g >> 2) + f(w), f = 0 1 4 5 8 9 12 13, and place 8 g + w of V^T's
+// rows is the same key; P's columns follow by picking registers.  The 16-key
+// groups of a stage are 16 bytes further apart than their contents for the same reason.
+//
+// What bounds it: shared memory.  Per tile of 64 keys the table reads, the
+// stores, the staging and the norms take about 1400 cycles of the SM's
+// 128 bytes per cycle, the MMAs' B operands 512 more, against 1024 cycles of
+// matrix work.
+//
+// Every wait is bounded (wait_limit_ns from its own beginning), after which the
+// kernel raises HLWQ_DEVERR_TIMEOUT, drains its copies and MMAs and frees its
+// tensor memory.
+
+#include <type_traits>
+
+#include "gemm_tc.cuh"
+#include "kvattn.cuh"
+
+namespace hlwq {
+
+namespace {
+
+constexpr int kAtRows = 128;
+constexpr int kAtWarps = 14, kAtThreads = 32 * kAtWarps;
+constexpr int kAtDec0 = 4, kAtMma = 12, kAtLoad = 13;
+constexpr int kGrp = 1536 + 16;                      // 16 keys' codes, and the gap
+constexpr int kCodeStage = 12800;                    // K codes, V codes, norms [2][64] binary16, mask
+constexpr int kCodeStages = 3;
+constexpr int kNormOff = 2 * 4 * kGrp;               // 12416
+constexpr int kMaskOff = kNormOff + 256;
+constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
+constexpr int kNrmSlot = 128 * 4 + 16;               // K norms, V norms, maxima of V's, mask
+constexpr float kMinQm = 1e-36f;                     // a zero scale: masked keys (-inf) stay masked, the others equal
+constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
+constexpr int kAtSmem = 8192 /*align*/ + 8192 /*table*/ + 4 * kKvTile + kCodeStages * kCodeStage + 4 * kNrmSlot + 512;
+static_assert(kMaskOff + 4 <= kCodeStage, "code stage");
+static_assert(kAtSmem <= 227 * 1024, "shared memory");
+
+// Offset of key n of a tile (its row in the K tile, its score column).
+__host__ __device__ constexpr int at_key(int n) {
+  return 16 * (n & 3) + 2 * ((n >> 2) & 1) + ((n >> 3) & 1) + 4 * (n >> 4);
+}
+
+// Instruction descriptor: kind::f16 with binary16 or bfloat16 operands, K-major, D fp32, M = 128.
+__host__ __device__ constexpr uint32_t idesc_16(int n, bool bf16) {
+  return idesc_f16(n) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// Bounded wait whose limit starts when it has to wait.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity) {
+  uint64_t deadline = 0;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((n & 63u) == 0u) {
+      const uint64_t t = globaltimer_ns();
+      if (deadline == 0) deadline = t + wait_limit_ns();
+      else if (t > deadline) return false;
+    }
+  }
+}
+
+// The same for a whole warp: all lanes or none.
+__device__ __forceinline__ bool at_wait_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, at_wait(bar, parity));
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 64 columns of this warp's rows <-> registers.
+__device__ __forceinline__ void tc_ld64(uint32_t taddr, float (&v)[64]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[16];
+    tc_ld16(taddr + 16 * c, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[16 * c + i] = __uint_as_float(x[i]);
+  }
+  tc_wait_ld();
+}
+
+__device__ __forceinline__ void tc_st64(uint32_t taddr, const float (&v)[64]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(v[16 * c + i]);
+    tc_st16(taddr + 16 * c, x);
+  }
+}
+
+__device__ __forceinline__ void fwht64(float (&v)[64]) {
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+}
+
+// Second half of the 256-point transform of a row in O's columns, whose 64-column
+// blocks have been transformed: four values 64 apart at a time, 16 columns per
+// step; f(c, v) takes columns c + 64 k + i as v[16 k + i].
+template <class F>
+__device__ __forceinline__ void across_blocks(uint32_t row, F&& f) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16) {
+    float v[64];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t x[16];
+      tc_ld16(row + kColO + 64 * k + c, x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[16 * k + i] = __uint_as_float(x[i]);
+    }
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float p = v[i] + v[16 + i], q = v[i] - v[16 + i], r = v[32 + i] + v[48 + i], s = v[32 + i] - v[48 + i];
+      v[i] = p + r;
+      v[16 + i] = q + s;
+      v[32 + i] = p - r;
+      v[48 + i] = q - s;
+    }
+    f(c, v);
+  }
+}
+
+// One after another, the segments (item, range of its units) of a CTA's share.
+struct AtWalk {
+  int64_t u, u1, at, u0;
+  int pair;
+  KvItem it;
+  int h, ta, tb, e_tb;  // the segment: kv head, units [ta, tb), encoded ones [ta, e_tb)
+  __device__ __forceinline__ bool next(const KvAttn& a, int tiles) {
+    if (u >= u1) return false;
+    bool bad = false;
+    while (u >= at + static_cast<int64_t>(it.units) * a.H) {
+      at += static_cast<int64_t>(it.units) * a.H;
+      it = kv_item<kAtRows>(a, ++pair, tiles, bad);
+    }
+    h = static_cast<int>((u - at) / it.units);
+    ta = static_cast<int>(u - at - static_cast<int64_t>(h) * it.units);
+    tb = static_cast<int>(min(static_cast<int64_t>(it.units), ta + (u1 - u)));
+    e_tb = max(ta, min(tb, it.e_units));
+    u += tb - ta;
+    return true;
+  }
+};
+
+__global__ void __launch_bounds__(kAtThreads, 1)
+kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut* __restrict__ cuts) {
+  extern __shared__ __align__(16) uint8_t asm_raw[];
+  __shared__ int64_t warp_sums[kAtWarps], found[2];
+  pdl_trigger();
+  const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(asm_raw));
+  const uint32_t tab0 = (raw + 8191u) & ~8191u;
+  uint8_t* g0 = asm_raw + (tab0 - raw);
+  const uint32_t k_tiles = tab0 + 8192, v_tiles = k_tiles + 2 * kKvTile, codes = v_tiles + 2 * kKvTile;
+  const uint32_t nrm = codes + kCodeStages * kCodeStage, bars = nrm + 4 * kNrmSlot;
+  const uint32_t c_full = bars, c_empty = c_full + 8 * kCodeStages, k_full = c_empty + 8 * kCodeStages, k_empty = k_full + 16,
+                 v_full = k_empty + 16, v_empty = v_full + 16, s_full = v_empty + 16, p_full = s_full + 16,
+                 q_full = p_full + 16, o_done = q_full + 8, misc = o_done + 8;
+  volatile uint32_t* misc_g = reinterpret_cast<volatile uint32_t*>(g0 + (misc - tab0));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
+  int64_t mine0;
+  const int64_t U = kv_total_units<kAtRows, kAtThreads>(a, tiles, warp_sums, mine0);
+  const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));
+  if (static_cast<int>(blockIdx.x) >= ctas) return;  // before any barrier or tensor memory
+  AtWalk w;
+  w.u = w.u0 = kv_share(U, blockIdx.x, ctas);
+  w.u1 = kv_share(U, blockIdx.x + 1, ctas);
+  kv_find_unit<kAtRows, kAtThreads>(a, tiles, mine0, w.u0, found);
+  w.pair = static_cast<int>(found[0]);
+  w.at = found[1];
+  {
+    bool bad = false;
+    w.it = kv_item<kAtRows>(a, w.pair, tiles, bad);
+  }
+
+  kv_check_codebook(a.codebook);
+  for (int i = threadIdx.x; i < 64 * 32; i += kAtThreads)
+    reinterpret_cast<uint32_t*>(g0)[i] = pack_half2(__ldg(a.codebook + ((i >> 5) & 7)), __ldg(a.codebook + (i >> 8)));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kCodeStages; ++s) {
+      mbar_init(c_full + 8 * s, 1);
+      mbar_init(c_empty + 8 * s, 8);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full + 8 * s, 8);
+      mbar_init(k_empty + 8 * s, 1);
+      mbar_init(v_full + 8 * s, 8);
+      mbar_init(v_empty + 8 * s, 1);
+      mbar_init(s_full + 8 * s, 1);
+      mbar_init(p_full + 8 * s, 4);
+    }
+    mbar_init(q_full, 4);
+    mbar_init(o_done, 1);
+    fence_barrier_init();
+  }
+  if (warp == kAtMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc_g[0];
+  bool ok = true;
+
+  // Tiles are numbered through the CTA's whole share: gt, and ce for encoded ones.
+  // Ring slot and parity of tile j: j % 2 and (j / 2) & 1.
+  if (warp < kAtDec0) {
+    // ------------------------------------------------------------ softmax
+    const int r = threadIdx.x;  // row of the tile
+    const uint32_t row = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const float sgn = a.scale < 0.0f ? -1.0f : 1.0f;
+    uint32_t gt = 0;
+    while (ok && w.next(a, tiles)) {
+      const KvItem& it = w.it;
+      const bool on = r < it.nrows;
+      const int tr = it.row0 + (on ? r : 0), tok = tr / a.G, head = w.h * a.G + (tr - tok * a.G);
+      const uint16_t* qrow = a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + head * kKvDim;
+      const int lim = on ? it.p + tok + 1 : 0;
+      if (r == 0 && w.ta > 0 && w.u - (w.tb - w.ta) == w.u0) {
+        const int64_t s0 = w.at + static_cast<int64_t>(w.h) * it.units, s1 = s0 + it.units;
+        int count = 0;
+        if (kv_share(U, blockIdx.x - 1, ctas) <= s0)
+          count = 1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - blockIdx.x;
+        cuts[blockIdx.x] = {count, it.b, w.h, it.row0};
+      }
+      float m = kMinM, l = 0.0f, fv = 2147483648.0f, qm = 0.0f;
+      bool started = false;  // O holds something
+
+      // One tile: S(gt) -> P(gt).  kWin: window keys, p in two bf16 parts.
+      auto tile = [&](auto win, int k0, int end) -> bool {
+        constexpr bool kWin = decltype(win)::value;
+        const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
+        const uint32_t sc = row + kColS + 64 * s, nb = nrm + (gt & 3u) * kNrmSlot;
+        if (!at_wait_warp(s_full + 8 * s, par)) return false;
+        tc_fence_after();
+        float v[64];
+        tc_ld64(sc, v);
+        if constexpr (!kWin) {
+#pragma unroll
+          for (int n = 0; n < 64; n += 4) {
+            const float4 x = lds_f4(nb + 4 * n);
+            v[n] *= x.x;
+            v[n + 1] *= x.y;
+            v[n + 2] *= x.z;
+            v[n + 3] *= x.w;
+          }
+        }
+        const uint32_t there = kWin ? 15u : lds32(nb + 520);  // 16-key groups whose page is there
+        const int see = min(lim, end) - k0;
+        if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
+#pragma unroll
+          for (int n = 0; n < 64; ++n)
+            if (at_key(n) >= see || !((there >> (n & 3)) & 1u)) v[n] = -INFINITY;
+        }
+        float mx = v[0];
+#pragma unroll
+        for (int n = 1; n < 64; ++n) mx = fmaxf(mx, v[n]);
+        mx *= qm;
+        float corr = 1.0f;
+        bool fix = false;
+        if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
+          const float nm = fmaxf(m, mx);
+          corr = exp2f(m - nm);
+          m = nm;
+          l *= corr;
+          fix = true;
+        }
+        if constexpr (!kWin) {
+          const float vm = __uint_as_float(max(lds32(nb + 512), lds32(nb + 516)));
+          if (vm * fv > 128.0f) {  // the same for all threads
+            const int e = min(144, static_cast<int>(__float_as_uint(vm) >> 23) + 1);
+            const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23);
+            corr *= nf / fv;
+            fv = nf;
+            fix = true;
+          }
+        }
+        if (fix && started) {  // rescale O once the product before has been added
+          if (!at_wait_warp(o_done, (gt - 1) & 1u)) return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t x[16], y[16];
+            tc_ld16(row + kColO + c, x);
+            tc_ld16(row + kColO + c + 16, y);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              x[i] = __float_as_uint(__uint_as_float(x[i]) * corr);
+              y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+            }
+            tc_st16(row + kColO + c, x);
+            tc_st16(row + kColO + c + 16, y);
+          }
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 64; ++n) {
+          v[n] = exp2f(fmaf(v[n], qm, -m));
+          sum += v[n];
+        }
+        l += sum;
+        if constexpr (!kWin) {
+#pragma unroll
+          for (int n = 0; n < 64; n += 4) {
+            const float4 x = lds_f4(nb + 256 + 4 * n);
+            v[n] *= x.x * fv;
+            v[n + 1] *= x.y * fv;
+            v[n + 2] *= x.z * fv;
+            v[n + 3] *= x.w * fv;
+          }
+          // place 8 g + i of V's rows is the key of score column 8 i + g
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int g = 4 * c + (i >> 2), j = 2 * (i & 3);
+              x[i] = pack_half2(v[8 * j + g], v[8 * j + 8 + g]);
+            }
+            tc_st16(sc + 16 * c, x);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int g = 4 * c + (i >> 2), j = 2 * (i & 3);
+              hi[i] = pack_bf162(v[8 * j + g], v[8 * j + 8 + g]);
+              lo[i] = pack_bf162(v[8 * j + g] - bf16x2_lo(hi[i]), v[8 * j + 8 + g] - bf16x2_hi(hi[i]));
+            }
+            tc_st16(sc + 16 * c, hi);
+            tc_st16(sc + 32 + 16 * c, lo);
+          }
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * s);
+        started = true;
+        ++gt;
+        return true;
+      };
+
+      if (w.ta < w.e_tb) {
+        // Q, rotated: blocks of 64 dims, then across the blocks, into binary16
+        float ss = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float v[64];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (on) x = __ldg(reinterpret_cast<const uint4*>(qrow + 64 * c) + i);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[8 * i + 2 * k] = bf16x2_lo(xs[k]), v[8 * i + 2 * k + 1] = bf16x2_hi(xs[k]);
+          }
+#pragma unroll
+          for (int i = 0; i < 64; ++i) ss = fmaf(v[i], v[i], ss);
+          fwht64(v);
+          tc_st64(row + kColO + 64 * c, v);
+        }
+        tc_wait_st();
+        float inv;
+        // |q H| <= 16 |q|: with |q| brought into [16, 32) no coordinate passes 512
+        const float sc = sgn * pow2_scale(sqrtf(ss), inv);
+        qm = fmaxf(fabsf(a.scale) * inv * (kLog2e / 256.0f), kMinQm);
+        across_blocks(row, [&](int c, const float(&v)[64]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = pack_half2(v[16 * k + 2 * i] * sc, v[16 * k + 2 * i + 1] * sc);
+            tc_st8(row + kColQ + 32 * k + (c >> 1), x);
+          }
+        });
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        for (int t = w.ta; ok && t < w.e_tb; ++t) ok = tile(std::false_type{}, t * kUnit, it.e_lim);
+        if (ok) ok = at_wait_warp(o_done, (gt - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        // O out of the rotated domain
+        const float f = 1.0f / (256.0f * fv);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float v[64];
+          tc_ld64(row + kColO + 64 * c, v);
+          fwht64(v);
+          tc_st64(row + kColO + 64 * c, v);
+        }
+        tc_wait_st();
+        across_blocks(row, [&](int c, const float(&v)[64]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(v[16 * k + i] * f);
+            tc_st16(row + kColO + 64 * k + c, x);
+          }
+        });
+        tc_wait_st();
+      }
+      if (w.e_tb < w.tb) {
+        // window units: Q as it is
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t x[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (on) y = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * c) + i);
+            const uint32_t flip = sgn < 0.0f ? 0x80008000u : 0u;
+            x[4 * i] = y.x ^ flip, x[4 * i + 1] = y.y ^ flip, x[4 * i + 2] = y.z ^ flip, x[4 * i + 3] = y.w ^ flip;
+          }
+          tc_st16(row + kColQ + 16 * c, x);
+        }
+        tc_wait_st();
+        qm = fmaxf(fabsf(a.scale) * kLog2e, kMinQm);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        for (int t = w.e_tb; ok && t < w.tb; ++t) ok = tile(std::true_type{}, it.e_lim + (t - it.e_units) * kUnit, it.w_lim);
+        if (ok) ok = at_wait_warp(o_done, (gt - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // the rows, or their part
+      const bool whole = w.ta == 0 && w.tb == it.units;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t* orow = a.out + static_cast<int64_t>(it.c0 + tok) * a.ldo + head * kKvDim;
+      float* part = parts + static_cast<int64_t>(2 * blockIdx.x + (w.ta == 0 ? 1 : 0)) * (kAtRows * (kKvDim + 2));
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t x[32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t y[16];
+          tc_ld16(row + kColO + c + 16 * k, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[16 * k + i] = y[i];
+        }
+        tc_wait_ld();
+        if (on && whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = pack_bf162(__uint_as_float(x[8 * k + 2 * i]) * inv, __uint_as_float(x[8 * k + 2 * i + 1]) * inv);
+            reinterpret_cast<uint4*>(orow + c)[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (on) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // [64 columns / 4][row][4]: a warp writes 512 bytes at a time
+            reinterpret_cast<uint4*>(part)[(c / 4 + k) * kAtRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+      if (!whole && on) {
+        part[kAtRows * kKvDim + r] = m;
+        part[kAtRows * (kKvDim + 1) + r] = l;
+      }
+    }
+  } else if (warp < kAtMma) {
+    // ------------------------------------------------------------ decode
+    const int dw = warp - kAtDec0, g = lane & 7, t4 = lane >> 3, tid = threadIdx.x - 32 * kAtDec0;
+    const uint32_t tab = tab0 + 4 * lane;
+    uint32_t gt = 0, ce = 0;
+    while (ok && w.next(a, tiles)) {
+      for (int t = w.ta; ok && t < w.e_tb; ++t, ++gt, ++ce) {
+        const uint32_t cs = ce % kCodeStages, st = codes + cs * kCodeStage, s = gt & 1u, par = (gt >> 1) & 1u;
+        ok = at_wait_warp(c_full + 8 * cs, (ce / kCodeStages) & 1u) && at_wait_warp(k_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        const uint32_t there = lds32(st + kMaskOff);
+        const int left = w.it.e_lim - t * kUnit;  // keys from here to the end
+        if (tid < 128) {
+          const int n = tid & 63, key = at_key(n);
+          const uint32_t wd = lds32(st + kNormOff + (tid >> 6) * 128 + 4 * (key >> 1));
+          float x = half_bits_to_float(static_cast<uint16_t>(wd >> (16 * (key & 1))));
+          if (key >= left || !((there >> (key >> 4)) & 1u)) x = 0.0f;
+          const uint32_t slot = nrm + (gt & 3u) * kNrmSlot;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + 4 * tid), "f"(x) : "memory");
+          const uint32_t mx = __reduce_max_sync(0xffffffffu, x == x ? __float_as_uint(x) : 0u);
+          if (dw >= 2 && lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 512 + 4 * (dw - 2)), "r"(mx) : "memory");
+          if (tid == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 520), "r"(there) : "memory");
+        }
+        {  // K: key of row 8 dw + g, dims 64 t4 .. + 63
+          const uint32_t src = st + (g & 3) * kGrp + (2 * (g >> 2) + (dw & 1) + 4 * (dw >> 1)) * kKvBytes + 24 * t4;
+          uint32_t x[6];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint2 y = lds64(src + 8 * i);
+            x[2 * i] = y.x, x[2 * i + 1] = y.y;
+          }
+          const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int bit = 24 * c + 6 * k, wi = bit >> 5, sh = bit & 31;
+              uint32_t y;
+              if (sh > 26) y = __funnelshift_r(x[wi], x[wi + 1], sh - 7);
+              else if (sh >= 7) y = x[wi] >> (sh - 7);
+              else y = x[wi] << (7 - sh);
+              h[k] = lds32((y & 0x1f80u) | tab);
+            }
+            sts128(dst + ((c ^ g) << 4), h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + 8 * s);
+        ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        {  // V^T: places 8 g .. + 7, dims 8 (4 dw + t4) .. + 7: 24 bits of each of eight keys
+          const uint32_t src = st + 4 * kGrp + (g & 3) * kGrp + 2 * (g >> 2) * kKvBytes + 12 * dw + 4 * ((24 * t4) >> 5);
+          uint32_t x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t at = src + ((i & 1) + 4 * (i >> 1)) * kKvBytes;
+            x[i] = __funnelshift_r(lds32(at), lds32(at + 4), (24 * t4) & 31);
+          }
+          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
+          constexpr uint32_t kEven = 0x1c71c7u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // even and odd codes of two keys side by side
+            const uint32_t p = x[2 * i], q = x[2 * i + 1];
+            x[2 * i] = (p & kEven) | ((q << 3) & ~kEven);
+            x[2 * i + 1] = ((p >> 3) & kEven) | (q & ~kEven);
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t y = x[2 * i + (c & 1)];
+              const int sh = 6 * (c >> 1);
+              h[i] = lds32(((sh >= 7 ? y >> (sh - 7) : y << (7 - sh)) & 0x1f80u) | tab);
+            }
+            sts128(dst + c * 128 + ((g ^ c) << 4), h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v_full + 8 * s);
+          mbar_arrive(c_empty + 8 * cs);
+        }
+      }
+      if (!ok) break;
+      const int R = static_cast<int>(a.R);
+      const int64_t ring = (static_cast<int64_t>(w.it.b) * a.H + w.h) * R;
+      for (int t = w.e_tb; ok && t < w.tb; ++t, ++gt) {
+        const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
+        const int k0 = w.it.e_lim + (t - w.it.e_units) * kUnit, end = w.it.w_lim;
+        ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        {
+          const int key = k0 + at_key(8 * dw + g);
+          const uint4* src = reinterpret_cast<const uint4*>(a.kwin + (ring + (key < end ? key % R : 0)) * kKvDim + 64 * t4);
+          const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (key < end) x = __ldg(src + c);
+            sts128(dst + ((c ^ g) << 4), x.x, x.y, x.z, x.w);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + 8 * s);
+        ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        {
+          uint32_t x[8][4];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = k0 + at_key(8 * i + g);
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (key < end) y = __ldg(reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 8 * (4 * dw + t4)));
+            x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+          }
+          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __byte_perm(x[2 * i][c >> 1], x[2 * i + 1][c >> 1], (c & 1) ? 0x7632 : 0x5410);
+            sts128(dst + c * 128 + ((g ^ c) << 4), h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + 8 * s);
+      }
+    }
+  } else if (warp == kAtMma) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      uint32_t gt = 0, nq = 0;
+      // O (+)= P(j) V(j)
+      auto pv = [&](uint32_t j, bool win, bool first) -> bool {
+        const uint32_t s = j & 1u, par = (j >> 1) & 1u;
+        if (!at_wait(v_full + 8 * s, par) || !at_wait(p_full + 8 * s, par)) return false;
+        tc_fence_after();
+        const uint64_t desc = smem_desc_sw128(v_tiles + s * kKvTile);
+        const uint32_t id = idesc_16(256, win);
+        for (int part = 0; part < (win ? 2 : 1); ++part)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_f16(tmem + kColO, tmem + kColS + 64 * s + 32 * part + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
+                       first && part == 0 && k == 0 ? 0u : 1u);
+        tc_commit(v_empty + 8 * s);
+        tc_commit(o_done);
+        return true;
+      };
+      while (ok && w.next(a, tiles)) {
+        bool first = true;
+        for (int phase = 0; ok && phase < 2; ++phase) {
+          const bool win = phase == 1;
+          const int n = win ? w.tb - w.e_tb : w.e_tb - w.ta;
+          if (n == 0) continue;
+          ok = at_wait(q_full, nq & 1u);
+          ++nq;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t id = idesc_16(64, win);
+          for (int t = 0; ok && t < n; ++t, ++gt) {
+            const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
+            ok = at_wait(k_full + 8 * s, par);
+            if (!ok) break;
+            tc_fence_after();
+            // S(gt)'s columns were P(gt - 2): its product was issued before
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint64_t desc = smem_desc_sw128(k_tiles + s * kKvTile + 8192 * c);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma_f16(tmem + kColS + 64 * s, tmem + kColQ + 32 * c + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
+                           c || k ? 1u : 0u);
+            }
+            tc_commit(k_empty + 8 * s);
+            tc_commit(s_full + 8 * s);
+            if (t > 0) {
+              ok = pv(gt - 1, win, first);
+              first = false;
+            }
+          }
+          if (ok) {
+            ok = pv(gt - 1, win, first);
+            first = false;
+          }
+        }
+      }
+      if (ok && gt > 0) {  // the last commits' arrivals land before the CTA ends
+        at_wait(k_empty + 8 * ((gt - 1) & 1u), ((gt - 1) >> 1) & 1u);
+        at_wait(v_empty + 8 * ((gt - 1) & 1u), ((gt - 1) >> 1) & 1u);
+      }
+      if (!ok) {
+        // no MMA may be under way when the tensor memory is freed: one more commit, waited for
+        mbar_init(misc + 16, 1);
+        fence_barrier_init();
+        tc_commit(misc + 16);
+        at_wait(misc + 16, 0);
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  } else {
+    // ------------------------------------------------------------ loader
+    uint32_t ce = 0;
+    while (ok && w.next(a, tiles)) {
+      for (int t = w.ta; ok && t < w.e_tb; ++t) {
+        const uint32_t cs = ce % kCodeStages, st = codes + cs * kCodeStage, bar = c_full + 8 * cs;
+        ok = at_wait_warp(c_empty + 8 * cs, ((ce / kCodeStages) & 1u) ^ 1u);
+        if (!ok) break;
+        if (fault_skip_tma()) {
+          ++ce;
+          continue;
+        }
+        // lane = 4 kind + group: codes of K, codes of V, norms of K, norms of V
+        const int grp = lane & 3, kind = lane >> 2, key = t * kUnit + 16 * grp;
+        bool there = false;
+        int64_t row_ = 0;
+        if (lane < 16 && key < w.it.e_lim) {
+          const int kp = key / static_cast<int>(a.P);
+          const int page = kp < a.max_pages ? __ldg(a.table + w.it.b * a.max_pages + kp) : -1;
+          there = page >= 0 && page < a.num_pages;
+          if (!there) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+          row_ = (static_cast<int64_t>(page) * a.H + w.h) * a.P + (key - kp * static_cast<int>(a.P));
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, there);
+        if (lane == 0) {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + kMaskOff), "r"(mask & 15u) : "memory");
+          mbar_arrive_expect_tx(bar, __popc(mask & 15u) * 2 * (1536 + 32));
+        }
+        __syncwarp();
+        if (there) {
+          if (kind == 0) bulk_load(st + grp * kGrp, a.kp + row_ * kKvBytes, 1536, bar);
+          else if (kind == 1) bulk_load(st + 4 * kGrp + grp * kGrp, a.vp + row_ * kKvBytes, 1536, bar);
+          else if (kind == 2) bulk_load(st + kNormOff + 32 * grp, a.kn + row_, 32, bar);
+          else bulk_load(st + kNormOff + 128 + 32 * grp, a.vn + row_, 32, bar);
+        }
+        ++ce;
+      }
+    }
+    // no copy may be landing when the CTA ends: the last ones issued into each stage
+    if (!fault_skip_tma())
+      for (uint32_t j = ce > kCodeStages ? ce - kCodeStages : 0; j < ce; ++j)
+        at_wait_warp(c_full + 8 * (j % kCodeStages), (j / kCodeStages) & 1u);
+  }
+  if (!ok && lane == 0) raise_device_error(HLWQ_DEVERR_TIMEOUT);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kAtMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+int launch_tiles(const KvAttn& a, int ctas, int tiles, float* parts, KvCut* cuts, cudaStream_t stream) {
+  static PerDeviceOnce attr;
+  if (const int st = attr([&] {
+        return cudaFuncSetAttribute(kv_attn_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem) ==
+               cudaSuccess;
+      }))
+    return st;
+  kv_attn_tile_kernel<<<ctas, kAtThreads, kAtSmem, stream>>>(a, tiles, parts, cuts);
+  if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
+  return launch_join<kAtRows>(a, ctas, parts, cuts, stream);
+}
+
+// Rows per tile, CTAs and row tiles of a request for max_new new tokens: the
+// few-row kernel up to 16 rows per kv head, the tensor-core tiles above.
+struct KvGrid {
+  int rows, ctas;
+  int64_t tiles;
+};
+inline KvGrid kv_grid(int64_t max_new, int64_t G) {
+  const int64_t n = max_new * G;
+  const int rows = n <= 8 ? 8 : n <= 16 ? 16 : kAtRows;
+  return {rows, sm_count() * (rows == 8 ? RowCfg<1>::kCtas : rows == 16 ? RowCfg<2>::kCtas : 1), ceil_div(n, rows)};
+}
+
+}  // namespace
+
+// Workspace: two partial results per CTA, then a note per CTA for the join.
+size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t Hq, int64_t H) {
+  const KvGrid gr = kv_grid(max_new, Hq / H);
+  return static_cast<size_t>(gr.ctas) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
+}
+
+int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
+  const KvGrid gr = kv_grid(max_new, a.G);
+  if (gr.tiles * a.B > INT32_MAX) return HLWQ_EUNSUPPORTED;
+  const int tiles = static_cast<int>(gr.tiles);
+  float* parts = static_cast<float*>(workspace);
+  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.ctas * gr.rows * (kKvDim + 2));
+  return gr.rows == 8    ? launch_rows<1>(a, gr.ctas, tiles, parts, cuts, stream)
+         : gr.rows == 16 ? launch_rows<2>(a, gr.ctas, tiles, parts, cuts, stream)
+                         : launch_tiles(a, gr.ctas, tiles, parts, cuts, stream);
+}
+
+}  // namespace hlwq
