@@ -170,6 +170,13 @@ __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
+// 2^x, one instruction (relative error below 2^-22; results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -452,7 +459,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float f = exp2f(m[nt][k] - x);
+            const float f = ex2(m[nt][k] - x);
             m[nt][k] = x;
             l[nt][k] *= f;
 #pragma unroll
@@ -466,7 +473,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[nt][k] = exp2f(d[nt][k] - m[nt][k & 1]);
+        for (int k = 0; k < 4; ++k) d[nt][k] = ex2(d[nt][k] - m[nt][k & 1]);
         l[nt][0] += d[nt][0] + d[nt][2];
         l[nt][1] += d[nt][1] + d[nt][3];
       }
@@ -711,7 +718,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         float x = mstat[0][r];
 #pragma unroll
         for (int w = 1; w < kRowWarps; ++w) x = fmaxf(x, mstat[w][r]);
-        const float f = exp2f(m[nt][k] - x);
+        const float f = ex2(m[nt][k] - x);
         // [row tile][row parity][tile m, dim parity][lane]
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -737,7 +744,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
       for (int w = 1; w < kRowWarps; ++w) mx = fmaxf(mx, mstat[w][r]);
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) sum += lstat[w][r] * exp2f(mstat[w][r] - mx);
+      for (int w = 0; w < kRowWarps; ++w) sum += lstat[w][r] * ex2(mstat[w][r] - mx);
       if (ta == 0 && tb == it.units) {
         if (r < nrows) {
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -800,7 +807,7 @@ kv_attn_join_kernel(const KvAttn a, const float* __restrict__ parts, const KvCut
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   auto add = [&](float pm, float pl, const float (&x)[8]) {
-    const float nm = fmaxf(m, pm), fo = exp2f(m - nm), fn = exp2f(pm - nm);
+    const float nm = fmaxf(m, pm), fo = ex2(m - nm), fn = ex2(pm - nm);
     m = nm;
     l = l * fo + pl * fn;
 #pragma unroll

@@ -11,16 +11,18 @@
 // decoded); K [64 keys][256 dims] and V^T [256 dims][64 keys] are the B operands,
 // both K-major with the 128-byte swizzle, decoded there from the 3-bit codes.
 //
-// Roles (14 warps):
-//   0..3   softmax: thread = row.  Puts Q into tensor memory (rotated per thread,
-//          in two passes over the columns of O, which are free then), turns S(j)
-//          into P(j), rescales O when a row's reference rises (seldom, as in the
-//          few-row kernel), rotates O back, writes the rows.
-//   4..11  decode: code pairs -> binary16 pairs through the 64-entry table (one
+// Roles (18 warps):
+//   0..7   softmax: two threads per row (warps q and q + 4 of tensor-memory quarter
+//          q), half the columns each.  They put Q into tensor memory (rotated in
+//          two passes over the columns of O, which are free then), turn S(j) into
+//          P(j), rescale O when a row's reference rises (seldom, as in the few-row
+//          kernel; one reducing barrier of the two warps finds out), rotate O back
+//          and write the rows.
+//   8..15  decode: code pairs -> binary16 pairs through the 64-entry table (one
 //          copy per lane) -> 16-byte stores into the K and V^T tiles; window
 //          tiles are copied (K) and transposed (V) as they are, bf16.
-//   12     issues the MMAs: S(j + 1), then O += P(j) V(j).
-//   13     fetches codes and norms, 16 keys (never two pages) per bulk copy.
+//   16     issues the MMAs: S(j + 1), then O += P(j) V(j).
+//   17     fetches codes and norms, 16 keys (never two pages) per bulk copy.
 //
 // Keys stand in the tiles in an order that keeps every shared-memory access of
 // the decoders free of bank conflicts: row n = 8 w + g of the K tile is key
@@ -47,8 +49,8 @@ namespace hlwq {
 namespace {
 
 constexpr int kAtRows = 128;
-constexpr int kAtWarps = 14, kAtThreads = 32 * kAtWarps;
-constexpr int kAtDec0 = 4, kAtMma = 12, kAtLoad = 13;
+constexpr int kAtWarps = 18, kAtThreads = 32 * kAtWarps;
+constexpr int kAtDec0 = 8, kAtMma = 16;
 constexpr int kGrp = 1536 + 16;                      // 16 keys' codes, and the gap
 constexpr int kCodeStage = 12800;                    // K codes, V codes, norms [2][64] binary16, mask
 constexpr int kCodeStages = 3;
@@ -58,7 +60,8 @@ constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
 constexpr int kNrmSlot = 128 * 4 + 16;               // K norms, V norms, maxima of V's, mask
 constexpr float kMinQm = 1e-36f;                     // a zero scale: masked keys (-inf) stay masked, the others equal
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
-constexpr int kAtSmem = 8192 /*align*/ + 8192 /*table*/ + 4 * kKvTile + kCodeStages * kCodeStage + 4 * kNrmSlot + 512;
+constexpr int kAtSmem = 8192 /*align*/ + 8192 /*table*/ + 4 * kKvTile + kCodeStages * kCodeStage + 4 * kNrmSlot + 512 +
+                        2 * kAtRows * 4 /*row exchange*/;
 static_assert(kMaskOff + 4 <= kCodeStage, "code stage");
 static_assert(kAtSmem <= 227 * 1024, "shared memory");
 
@@ -120,6 +123,13 @@ __device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+__device__ __forceinline__ void tc_ld4(uint32_t taddr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr)
+               : "memory");
+}
+
 // 64 columns of this warp's rows <-> registers.
 __device__ __forceinline__ void tc_ld64(uint32_t taddr, float (&v)[64]) {
 #pragma unroll
@@ -154,13 +164,50 @@ __device__ __forceinline__ void fwht64(float (&v)[64]) {
       }
 }
 
-// Second half of the 256-point transform of a row in O's columns, whose 64-column
-// blocks have been transformed: four values 64 apart at a time, 16 columns per
-// step; f(c, v) takes columns c + 64 k + i as v[16 k + i].
-template <class F>
-__device__ __forceinline__ void across_blocks(uint32_t row, F&& f) {
+// The two warps of a tensor-memory quarter: barrier 1 + quarter, 64 threads.
+__device__ __forceinline__ void pair_sync(int quarter) {
+  tc_fence_before();
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+  tc_fence_after();
+}
+
+// Whether x holds for any thread of the two warps (a barrier for both).  A warp whose
+// wait ran out tells the other one here before it gives up, so that
+// neither is left at a barrier.
+__device__ __forceinline__ bool pair_any(int quarter, bool x) {
+  uint32_t y;
+  tc_fence_before();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(x ? 1u : 0u), "r"(1 + quarter)
+      : "memory");
+  tc_fence_after();
+  return y != 0u;
+}
+
+// The 64-column blocks 2 half, 2 half + 1 of the 256-point transform of a row in O's columns.
+__device__ __forceinline__ void within_blocks(uint32_t row, int half) {
 #pragma unroll 1
-  for (int c = 0; c < 64; c += 16) {
+  for (int c = 0; c < 2; ++c) {
+    float v[64];
+    tc_ld64(row + kColO + 128 * half + 64 * c, v);
+    fwht64(v);
+    tc_st64(row + kColO + 128 * half + 64 * c, v);
+  }
+  tc_wait_st();
+}
+
+// Then across the blocks: four values 64 columns apart at a time, 16 columns per
+// step, columns 32 half .. + 31 of each block; f(c, v) takes column c + 64 k + i
+// as v[16 k + i].
+template <class F>
+__device__ __forceinline__ void across_blocks(uint32_t row, int half, F&& f) {
+#pragma unroll 1
+  for (int c = 32 * half; c < 32 * half + 32; c += 16) {
     float v[64];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -180,6 +227,7 @@ __device__ __forceinline__ void across_blocks(uint32_t row, F&& f) {
     }
     f(c, v);
   }
+  tc_wait_st();
 }
 
 // One after another, the segments (item, range of its units) of a CTA's share.
@@ -250,9 +298,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       mbar_init(v_full + 8 * s, 8);
       mbar_init(v_empty + 8 * s, 1);
       mbar_init(s_full + 8 * s, 1);
-      mbar_init(p_full + 8 * s, 4);
+      mbar_init(p_full + 8 * s, 8);
     }
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     mbar_init(o_done, 1);
     fence_barrier_init();
   }
@@ -270,9 +318,11 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   // Ring slot and parity of tile j: j % 2 and (j / 2) & 1.
   if (warp < kAtDec0) {
     // ------------------------------------------------------------ softmax
-    const int r = threadIdx.x;  // row of the tile
-    const uint32_t row = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int half = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;  // r: row of the tile
+    const uint32_t row = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float sgn = a.scale < 0.0f ? -1.0f : 1.0f;
+    float* mine = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + half * kAtRows + r;        // exchange with the
+    const float* other = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + (half ^ 1) * kAtRows + r;  // row's other thread
     uint32_t gt = 0;
     while (ok && w.next(a, tiles)) {
       const KvItem& it = w.it;
@@ -280,123 +330,146 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       const int tr = it.row0 + (on ? r : 0), tok = tr / a.G, head = w.h * a.G + (tr - tok * a.G);
       const uint16_t* qrow = a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + head * kKvDim;
       const int lim = on ? it.p + tok + 1 : 0;
-      if (r == 0 && w.ta > 0 && w.u - (w.tb - w.ta) == w.u0) {
+      if (threadIdx.x == 0 && w.ta > 0 && w.u - (w.tb - w.ta) == w.u0) {
         const int64_t s0 = w.at + static_cast<int64_t>(w.h) * it.units, s1 = s0 + it.units;
         int count = 0;
         if (kv_share(U, blockIdx.x - 1, ctas) <= s0)
           count = 1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - blockIdx.x;
         cuts[blockIdx.x] = {count, it.b, w.h, it.row0};
       }
-      float m = kMinM, l = 0.0f, fv = 2147483648.0f, qm = 0.0f;
+      // m: the row's reference; lf: log2 of the power of two that keeps p n in
+      // binary16's range, in l as in O; l: this thread's share of the row's sum
+      float m = kMinM, l = 0.0f, lf = 31.0f, qm = 0.0f;
       bool started = false;  // O holds something
 
-      // One tile: S(gt) -> P(gt).  kWin: window keys, p in two bf16 parts.
+      // One tile: S(gt) -> P(gt).  win: window keys, p in two bf16 parts.  This
+      // thread's score columns are 8 i + 4 half + k (i < 8, k < 4), v[i][k].
       auto tile = [&](auto win, int k0, int end) -> bool {
         constexpr bool kWin = decltype(win)::value;
         const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
-        const uint32_t sc = row + kColS + 64 * s, nb = nrm + (gt & 3u) * kNrmSlot;
-        if (!at_wait_warp(s_full + 8 * s, par)) return false;
+        const uint32_t sc = row + kColS + 64 * s, nb = nrm + (gt & 3u) * kNrmSlot + 16 * half;
+        const bool got = at_wait_warp(s_full + 8 * s, par);
         tc_fence_after();
-        float v[64];
-        tc_ld64(sc, v);
-        if constexpr (!kWin) {
+        float2 v[8][2];
+        {
+          uint32_t x[8][4];
 #pragma unroll
-          for (int n = 0; n < 64; n += 4) {
-            const float4 x = lds_f4(nb + 4 * n);
-            v[n] *= x.x;
-            v[n + 1] *= x.y;
-            v[n + 2] *= x.z;
-            v[n + 3] *= x.w;
+          for (int i = 0; i < 8; ++i) tc_ld4(sc + 8 * i + 4 * half, x[i]);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i][0] = make_float2(__uint_as_float(x[i][0]), __uint_as_float(x[i][1]));
+            v[i][1] = make_float2(__uint_as_float(x[i][2]), __uint_as_float(x[i][3]));
           }
         }
-        const uint32_t there = kWin ? 15u : lds32(nb + 520);  // 16-key groups whose page is there
+        if constexpr (!kWin) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 x = lds_f4(nb + 32 * i);
+            v[i][0] = fmul2(v[i][0], make_float2(x.x, x.y));
+            v[i][1] = fmul2(v[i][1], make_float2(x.z, x.w));
+          }
+        }
+        const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + 520);  // 16-key groups whose page is there
         const int see = min(lim, end) - k0;
         if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
+          const int sh = see - 2 * half;
 #pragma unroll
-          for (int n = 0; n < 64; ++n)
-            if (at_key(n) >= see || !((there >> (n & 3)) & 1u)) v[n] = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            const int f = at_key(8 * i);
+            if (f >= sh || !(there & 1u)) v[i][0].x = -INFINITY;
+            if (f + 16 >= sh || !(there & 2u)) v[i][0].y = -INFINITY;
+            if (f + 32 >= sh || !(there & 4u)) v[i][1].x = -INFINITY;
+            if (f + 48 >= sh || !(there & 8u)) v[i][1].y = -INFINITY;
+          }
         }
-        float mx = v[0];
+        float mx = fmaxf(fmaxf(v[0][0].x, v[0][0].y), fmaxf(v[0][1].x, v[0][1].y)), my = mx;
 #pragma unroll
-        for (int n = 1; n < 64; ++n) mx = fmaxf(mx, v[n]);
-        mx *= qm;
+        for (int i = 1; i < 8; ++i) {
+          mx = fmaxf(fmaxf(v[i][0].x, v[i][0].y), mx);
+          my = fmaxf(fmaxf(v[i][1].x, v[i][1].y), my);
+        }
+        mx = fmaxf(mx, my) * qm;
         float corr = 1.0f;
-        bool fix = false;
-        if (__any_sync(0xffffffffu, mx > m + 8.0f)) {
-          const float nm = fmaxf(m, mx);
-          corr = exp2f(m - nm);
+        // also: both halves of S have been read, P may take its place
+        bool fix = pair_any(quarter, !got || mx > m + 8.0f);
+        if (fix) {  // seldom
+          if (pair_any(quarter, !got)) return false;
+          *mine = mx;
+          pair_sync(quarter);
+          const float nm = fmaxf(m, fmaxf(mx, *other));
+          corr = ex2(m - nm);
           m = nm;
-          l *= corr;
-          fix = true;
+          pair_sync(quarter);
         }
         if constexpr (!kWin) {
-          const float vm = __uint_as_float(max(lds32(nb + 512), lds32(nb + 516)));
-          if (vm * fv > 128.0f) {  // the same for all threads
-            const int e = min(144, static_cast<int>(__float_as_uint(vm) >> 23) + 1);
-            const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23);
-            corr *= nf / fv;
-            fv = nf;
+          const float vm = __uint_as_float(max(lds32(nb - 16 * half + 512), lds32(nb - 16 * half + 516)));
+          if (vm * ex2(lf) > 128.0f) {  // the same for all threads
+            const int e = min(144, static_cast<int>(__float_as_uint(vm) >> 23) + 1);  // vm < 2^(e - 127)
+            corr *= ex2(static_cast<float>(132 - e) - lf);                            // vm 2^(132 - e) in [16, 32)
+            lf = static_cast<float>(132 - e);
             fix = true;
           }
         }
-        if (fix && started) {  // rescale O once the product before has been added
-          if (!at_wait_warp(o_done, (gt - 1) & 1u)) return false;
-          tc_fence_after();
+        if (fix) {
+          l *= corr;
+          if (started) {  // rescale O once the product before has been added
+            if (pair_any(quarter, !at_wait_warp(o_done, (gt - 1) & 1u))) return false;
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t x[16], y[16];
-            tc_ld16(row + kColO + c, x);
-            tc_ld16(row + kColO + c + 16, y);
-            tc_wait_ld();
+            for (int c = 128 * half; c < 128 * half + 128; c += 16) {
+              uint32_t x[16];
+              tc_ld16(row + kColO + c, x);
+              tc_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              x[i] = __float_as_uint(__uint_as_float(x[i]) * corr);
-              y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * corr);
+              tc_st16(row + kColO + c, x);
             }
-            tc_st16(row + kColO + c, x);
-            tc_st16(row + kColO + c + 16, y);
           }
         }
-        float sum = 0.0f;
+        // p 2^lf = 2^(s qm - m + lf), and its sum
+        const float2 q2 = make_float2(qm, qm), b2 = make_float2(lf - m, lf - m);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int n = 0; n < 64; ++n) {
-          v[n] = exp2f(fmaf(v[n], qm, -m));
-          sum += v[n];
-        }
-        l += sum;
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 x = fma2(v[i][k], q2, b2);
+            v[i][k] = make_float2(ex2(x.x), ex2(x.y));
+            sum[k] = add2(sum[k], v[i][k]);
+          }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        // place 8 g + i of V's rows is the key of score column 8 i + g; word (g, i / 2)
         if constexpr (!kWin) {
 #pragma unroll
-          for (int n = 0; n < 64; n += 4) {
-            const float4 x = lds_f4(nb + 256 + 4 * n);
-            v[n] *= x.x * fv;
-            v[n + 1] *= x.y * fv;
-            v[n + 2] *= x.z * fv;
-            v[n + 3] *= x.w * fv;
+          for (int i = 0; i < 8; ++i) {
+            const float4 x = lds_f4(nb + 256 + 32 * i);
+            v[i][0] = fmul2(v[i][0], make_float2(x.x, x.y));
+            v[i][1] = fmul2(v[i][1], make_float2(x.z, x.w));
           }
-          // place 8 g + i of V's rows is the key of score column 8 i + g
+          uint32_t x[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int g = 4 * c + (i >> 2), j = 2 * (i & 3);
-              x[i] = pack_half2(v[8 * j + g], v[8 * j + 8 + g]);
-            }
-            tc_st16(sc + 16 * c, x);
+          for (int i = 0; i < 4; ++i) {
+            x[i] = pack_half2(v[2 * i][0].x, v[2 * i + 1][0].x);
+            x[4 + i] = pack_half2(v[2 * i][0].y, v[2 * i + 1][0].y);
+            x[8 + i] = pack_half2(v[2 * i][1].x, v[2 * i + 1][1].x);
+            x[12 + i] = pack_half2(v[2 * i][1].y, v[2 * i + 1][1].y);
           }
+          tc_st16(sc + 16 * half, x);
         } else {
+          uint32_t hi[16], lo[16];
+          auto split = [&](int j, float x, float y) {
+            hi[j] = pack_bf162(x, y);
+            lo[j] = pack_bf162(x - bf16x2_lo(hi[j]), y - bf16x2_hi(hi[j]));
+          };
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int g = 4 * c + (i >> 2), j = 2 * (i & 3);
-              hi[i] = pack_bf162(v[8 * j + g], v[8 * j + 8 + g]);
-              lo[i] = pack_bf162(v[8 * j + g] - bf16x2_lo(hi[i]), v[8 * j + 8 + g] - bf16x2_hi(hi[i]));
-            }
-            tc_st16(sc + 16 * c, hi);
-            tc_st16(sc + 32 + 16 * c, lo);
+          for (int i = 0; i < 4; ++i) {
+            split(i, v[2 * i][0].x, v[2 * i + 1][0].x);
+            split(4 + i, v[2 * i][0].y, v[2 * i + 1][0].y);
+            split(8 + i, v[2 * i][1].x, v[2 * i + 1][1].x);
+            split(12 + i, v[2 * i][1].y, v[2 * i + 1][1].y);
           }
+          tc_st16(sc + 16 * half, hi);
+          tc_st16(sc + 32 + 16 * half, lo);
         }
         tc_wait_st();
         tc_fence_before();
@@ -408,10 +481,11 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       };
 
       if (w.ta < w.e_tb) {
-        // Q, rotated: blocks of 64 dims, then across the blocks, into binary16
+        // Q, rotated: this thread's two blocks of 64 dims, then its columns across
+        // the blocks, into binary16
         float ss = 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
           float v[64];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -427,11 +501,13 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           tc_st64(row + kColO + 64 * c, v);
         }
         tc_wait_st();
+        *mine = ss;
+        pair_sync(quarter);
         float inv;
         // |q H| <= 16 |q|: with |q| brought into [16, 32) no coordinate passes 512
-        const float sc = sgn * pow2_scale(sqrtf(ss), inv);
+        const float sc = sgn * pow2_scale(sqrtf(half ? *other + ss : ss + *other), inv);
         qm = fmaxf(fabsf(a.scale) * inv * (kLog2e / 256.0f), kMinQm);
-        across_blocks(row, [&](int c, const float(&v)[64]) {
+        across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t x[8];
@@ -440,25 +516,19 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             tc_st8(row + kColQ + 32 * k + (c >> 1), x);
           }
         });
-        tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         for (int t = w.ta; ok && t < w.e_tb; ++t) ok = tile(std::false_type{}, t * kUnit, it.e_lim);
-        if (ok) ok = at_wait_warp(o_done, (gt - 1) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        // O out of the rotated domain
-        const float f = 1.0f / (256.0f * fv);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float v[64];
-          tc_ld64(row + kColO + 64 * c, v);
-          fwht64(v);
-          tc_st64(row + kColO + 64 * c, v);
+        if (!ok || pair_any(quarter, !at_wait_warp(o_done, (gt - 1) & 1u))) {
+          ok = false;
+          break;
         }
-        tc_wait_st();
-        across_blocks(row, [&](int c, const float(&v)[64]) {
+        // O out of the rotated domain, and the sums with the same factor
+        within_blocks(row, half);
+        pair_sync(quarter);
+        const float f = ex2(-8.0f - lf);
+        across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t x[16];
@@ -467,12 +537,14 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             tc_st16(row + kColO + 64 * k + c, x);
           }
         });
-        tc_wait_st();
+        l *= ex2(-lf);
+        pair_sync(quarter);
       }
+      lf = 0.0f;
       if (w.e_tb < w.tb) {
         // window units: Q as it is
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 4 * half; c < 4 * half + 4; ++c) {
           uint32_t x[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -489,29 +561,27 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         for (int t = w.e_tb; ok && t < w.tb; ++t) ok = tile(std::true_type{}, it.e_lim + (t - it.e_units) * kUnit, it.w_lim);
-        if (ok) ok = at_wait_warp(o_done, (gt - 1) & 1u);
-        if (!ok) break;
-        tc_fence_after();
+        if (!ok || pair_any(quarter, !at_wait_warp(o_done, (gt - 1) & 1u))) {
+          ok = false;
+          break;
+        }
       }
-      // the rows, or their part
+      // the rows, or their part: this thread's half of the columns
+      *mine = l;
+      pair_sync(quarter);
+      l = half ? *other + l : l + *other;
       const bool whole = w.ta == 0 && w.tb == it.units;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       uint16_t* orow = a.out + static_cast<int64_t>(it.c0 + tok) * a.ldo + head * kKvDim;
       float* part = parts + static_cast<int64_t>(2 * blockIdx.x + (w.ta == 0 ? 1 : 0)) * (kAtRows * (kKvDim + 2));
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t x[32];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t y[16];
-          tc_ld16(row + kColO + c + 16 * k, y);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[16 * k + i] = y[i];
-        }
+      for (int c = 128 * half; c < 128 * half + 128; c += 16) {
+        uint32_t x[16];
+        tc_ld16(row + kColO + c, x);
         tc_wait_ld();
         if (on && whole) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             uint32_t y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -520,15 +590,16 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
         } else if (on) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // [64 columns / 4][row][4]: a warp writes 512 bytes at a time
+          for (int k = 0; k < 4; ++k)  // [256 columns / 4][row][4]: a warp writes 512 bytes at a time
             reinterpret_cast<uint4*>(part)[(c / 4 + k) * kAtRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
         __syncwarp();
       }
-      if (!whole && on) {
+      if (!whole && on && half == 0) {
         part[kAtRows * kKvDim + r] = m;
         part[kAtRows * (kKvDim + 1) + r] = l;
       }
+      pair_sync(quarter);  // O, Q and the exchange words are free for the next segment
     }
   } else if (warp < kAtMma) {
     // ------------------------------------------------------------ decode
