@@ -42,10 +42,11 @@ struct KvAttn {
 //
 // An item is (request, row tile, kv head): a row tile is kRows consecutive
 // (token, query head) rows of a request, row = token * G + g.  An item's keys are
-// cut into units (64 encoded tokens, or 64 window tokens); all items' units
-// in order, numbered 0 .. U - 1, are shared out evenly over the grid's CTAs in
-// contiguous ranges, whatever the requests' lengths are: one long request
-// is split over the machine, many short ones are not split.  Where a boundary
+// cut into units (64 encoded tokens, or 64 window tokens).  An item costs its units
+// and what beginning and ending it takes (rotations, the row's output), counted in
+// units.  All items' costs in order, 0 .. U - 1, are shared out evenly over the
+// grid's CTAs in contiguous ranges, whatever the requests' lengths are: one long
+// request is split over the machine, many short ones are not split.  Where a boundary
 // between two CTAs falls inside an item, its parts go to the workspace and
 // kv_attn_join_kernel adds them up.  Everything follows from cu and n_past, so every CTA
 // works its share out for itself: no plan is made beforehand and the host needs
@@ -64,11 +65,12 @@ struct KvItem {
   int e_lim;     // encoded tokens that the tile's last row sees
   int w_lim;     // tokens that it sees, window included
   int e_units, units;
+  int64_t cost;  // of all the kv heads' items of this pair; an item's own cost is cost / H
 };
 
 // The pair (request, row tile) number `pair`; units = 0 where it has no rows.
 // (T * q_heads and key positions are below 2^31: checked by the host and here.)
-template <int kRows>
+template <int kRows, int kItemCost>
 __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, bool& bad) {
   KvItem it;
   it.b = tiles == 1 ? pair : pair / tiles;
@@ -78,6 +80,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, 
   const int64_t n = static_cast<int64_t>(__ldg(a.cu + it.b + 1)) - it.c0;
   it.n = static_cast<int>(n);
   it.units = it.e_units = 0;
+  it.cost = 0;
   if (it.c0 < 0 || n < 0 || it.c0 + n > a.T || it.p < 0 || it.p + n > kMaxKeys) {
     bad = true;
     return it;
@@ -92,13 +95,14 @@ __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, 
   it.w_lim = sees;
   it.e_units = (it.e_lim + kUnit - 1) / kUnit;
   it.units = it.e_units + (it.w_lim - it.e_lim + kUnit - 1) / kUnit;
+  it.cost = static_cast<int64_t>(it.units + kItemCost) * a.H;
   return it;
 }
 
-// The total of all units; `mine0` = the units before this thread's pairs.  Called
+// The total of all costs; `mine0` = the cost before this thread's pairs.  Called
 // by all kThreads threads of the CTA.
-template <int kRows, int kThreads>
-__device__ __forceinline__ int64_t kv_total_units(const KvAttn& a, int tiles, int64_t* warp_sums, int64_t& mine0) {
+template <int kRows, int kItemCost, int kThreads>
+__device__ __forceinline__ int64_t kv_total_cost(const KvAttn& a, int tiles, int64_t* warp_sums, int64_t& mine0) {
   const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
@@ -107,7 +111,7 @@ __device__ __forceinline__ int64_t kv_total_units(const KvAttn& a, int tiles, in
   for (int i = 0; i < per; ++i) {
     const int pair = threadIdx.x * per + i;
     if (pair >= pairs) break;
-    sum += static_cast<int64_t>(kv_item<kRows>(a, pair, tiles, bad).units) * a.H;
+    sum += kv_item<kRows, kItemCost>(a, pair, tiles, bad).cost;
   }
   if (bad && blockIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
   int64_t inc = sum;
@@ -128,10 +132,10 @@ __device__ __forceinline__ int64_t kv_total_units(const KvAttn& a, int tiles, in
   return total;
 }
 
-// After kv_total_units: the pair holding unit `want`, found by the thread whose
-// pairs contain it and published in found[0] (pair) and found[1] (its first unit).
-template <int kRows, int kThreads>
-__device__ __forceinline__ void kv_find_unit(const KvAttn& a, int tiles, int64_t mine0, int64_t want, int64_t* found) {
+// After kv_total_cost: the pair holding cost `want`, found by the thread whose
+// pairs contain it and published in found[0] (pair) and found[1] (where its cost begins).
+template <int kRows, int kItemCost, int kThreads>
+__device__ __forceinline__ void kv_find(const KvAttn& a, int tiles, int64_t mine0, int64_t want, int64_t* found) {
   const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
   int64_t u = mine0;
   bool bad = false;
@@ -140,7 +144,7 @@ __device__ __forceinline__ void kv_find_unit(const KvAttn& a, int tiles, int64_t
     for (int i = 0; i < per; ++i) {
       const int pair = threadIdx.x * per + i;
       if (pair >= pairs) break;
-      const int64_t n = static_cast<int64_t>(kv_item<kRows>(a, pair, tiles, bad).units) * a.H;
+      const int64_t n = kv_item<kRows, kItemCost>(a, pair, tiles, bad).cost;
       if (want < u + n) {
         found[0] = pair;
         found[1] = u;
@@ -159,6 +163,57 @@ struct KvCut {
 };
 
 __device__ __forceinline__ int64_t kv_share(int64_t U, int c, int ctas) { return U * c / ctas; }
+
+// One after another, the segments (item, range of its units) of a CTA's share
+// [u0, u1) of the cost.  An item's first kItemCost are its beginning and end, then
+// comes a unit at each step: a boundary among the first ones cuts nothing.
+template <int kRows, int kItemCost>
+struct KvWalk {
+  int64_t u0, u, u1, at;  // share, where the walk is, where the pair's cost begins
+  int pair;
+  KvItem it;
+  int h, ta, tb, e_tb;    // the segment: kv head, units [ta, tb), encoded ones [ta, e_tb)
+
+  __device__ __forceinline__ void begin(const KvAttn& a, int tiles, int64_t U, int ctas, const int64_t* found) {
+    u = u0 = kv_share(U, blockIdx.x, ctas);
+    u1 = kv_share(U, blockIdx.x + 1, ctas);
+    pair = static_cast<int>(found[0]);
+    at = found[1];
+    bool bad = false;
+    it = kv_item<kRows, kItemCost>(a, pair, tiles, bad);
+  }
+  __device__ __forceinline__ bool next(const KvAttn& a, int tiles) {
+    bool bad = false;
+    while (u < u1) {
+      while (u >= at + it.cost) {
+        at += it.cost;
+        it = kv_item<kRows, kItemCost>(a, ++pair, tiles, bad);
+      }
+      const int each = it.units + kItemCost;
+      h = static_cast<int>((u - at) / each);
+      const int o = static_cast<int>(u - at - static_cast<int64_t>(h) * each);
+      const int n = static_cast<int>(min(static_cast<int64_t>(each - o), u1 - u));
+      u += n;
+      ta = max(0, o - kItemCost);
+      tb = max(0, o + n - kItemCost);
+      e_tb = max(ta, min(tb, it.e_units));
+      if (tb > ta) return true;
+    }
+    return false;
+  }
+  // The note for the join when this is the share's first segment and begins
+  // inside its item: whether the boundary before this CTA is the item's first cut.
+  __device__ __forceinline__ bool note(const KvAttn&, int64_t U, int ctas, KvCut& cut) const {
+    const int each = it.units + kItemCost;
+    const int64_t s0 = at + static_cast<int64_t>(h) * each, s1 = s0 + each;
+    if (ta == 0 || u0 <= s0) return false;
+    if (kv_share(U, blockIdx.x - 1, ctas) > s0 + kItemCost) return false;
+    // parts: the CTA before this one, this one, and those that begin before the item's end
+    cut = {1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - static_cast<int>(blockIdx.x), it.b,
+           h, it.row0};
+    return true;
+  }
+};
 
 // ---------------------------------------------------------------- building blocks
 
@@ -286,6 +341,7 @@ constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kStage = 3136;  // 16 keys: K codes 1536, V codes 1536, K norms 32, V norms 32
 constexpr int kStages = 4;
+constexpr int kRowItemCost = 2;
 constexpr int kTabBytes = 64 * 128;
 constexpr float kMinM = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -358,37 +414,20 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     reinterpret_cast<uint32_t*>(gtab)[i] = pack_half2(__ldg(a.codebook + ((i >> 5) & 7)), __ldg(a.codebook + (i >> 8)));
 
   int64_t mine0;
-  const int64_t U = kv_total_units<C::kRows, kRowThreads>(a, tiles, warp_sums, mine0);
+  const int64_t U = kv_total_cost<C::kRows, kRowItemCost, kRowThreads>(a, tiles, warp_sums, mine0);
   if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
-  const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));  // every one of these has work
+  const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));  // every one of these has a share
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const int64_t u0 = kv_share(U, blockIdx.x, ctas), u1 = kv_share(U, blockIdx.x + 1, ctas);
-  kv_find_unit<C::kRows, kRowThreads>(a, tiles, mine0, u0, found);
-  int pair = static_cast<int>(found[0]);
-  int64_t at = found[1];  // first unit of the pair
-  bool bad = false;
-  KvItem it = kv_item<C::kRows>(a, pair, tiles, bad);
+  kv_find<C::kRows, kRowItemCost, kRowThreads>(a, tiles, mine0, kv_share(U, blockIdx.x, ctas), found);
+  KvWalk<C::kRows, kRowItemCost> w;
+  w.begin(a, tiles, U, ctas, found);
 
-  for (int64_t u = u0; u < u1;) {
-    while (u >= at + static_cast<int64_t>(it.units) * a.H) {
-      at += static_cast<int64_t>(it.units) * a.H;
-      it = kv_item<C::kRows>(a, ++pair, tiles, bad);
-    }
-    const int h = static_cast<int>((u - at) / it.units);
-    const int ta = static_cast<int>(u - at - static_cast<int64_t>(h) * it.units);
-    const int tb = static_cast<int>(min(static_cast<int64_t>(it.units), ta + (u1 - u)));
-    u += tb - ta;
-    const int nrows = it.nrows;
-    if (threadIdx.x == 0 && ta > 0 && u == u0 + (tb - ta)) {
-      // this CTA begins inside an item: is the boundary before it the item's first cut?
-      const int64_t s0 = at + static_cast<int64_t>(h) * it.units;
-      int count = 0;
-      if (kv_share(U, blockIdx.x - 1, ctas) <= s0) {
-        // parts: the CTA before this one, this one, and those that begin before the item's end
-        const int64_t s1 = s0 + it.units;
-        count = 1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - blockIdx.x;
-      }
-      cuts[blockIdx.x] = {count, it.b, h, it.row0};
+  while (w.next(a, tiles)) {
+    const KvItem& it = w.it;
+    const int h = w.h, ta = w.ta, tb = w.tb, nrows = it.nrows;
+    if (threadIdx.x == 0) {
+      KvCut cut;
+      if (w.note(a, U, ctas, cut)) cuts[blockIdx.x] = cut;
     }
 
     // rotate the tile's rows into matrix-instruction order
@@ -480,7 +519,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     };
 
     // ---- encoded keys: tiles of 16, one warp each, kStages - 1 of them under way
-    const int e_tb = min(tb, it.e_units);
+    const int e_tb = w.e_tb;
     const int k_end = min(e_tb * kUnit, it.e_lim);
     const int k_first = ta * kUnit + 16 * warp;
     auto request = [&](int k0, int stage) {  // false: the page is not there

@@ -51,6 +51,7 @@ namespace {
 constexpr int kAtRows = 128;
 constexpr int kAtWarps = 18, kAtThreads = 32 * kAtWarps;
 constexpr int kAtDec0 = 8, kAtMma = 16;
+constexpr int kAtItemCost = 8;                       // units: an item takes about 12 us besides its tiles of 1.5 us
 constexpr int kGrp = 1536 + 16;                      // 16 keys' codes, and the gap
 constexpr int kCodeStage = 12800;                    // K codes, V codes, norms [2][64] binary16, mask
 constexpr int kCodeStages = 3;
@@ -230,28 +231,6 @@ __device__ __forceinline__ void across_blocks(uint32_t row, int half, F&& f) {
   tc_wait_st();
 }
 
-// One after another, the segments (item, range of its units) of a CTA's share.
-struct AtWalk {
-  int64_t u, u1, at, u0;
-  int pair;
-  KvItem it;
-  int h, ta, tb, e_tb;  // the segment: kv head, units [ta, tb), encoded ones [ta, e_tb)
-  __device__ __forceinline__ bool next(const KvAttn& a, int tiles) {
-    if (u >= u1) return false;
-    bool bad = false;
-    while (u >= at + static_cast<int64_t>(it.units) * a.H) {
-      at += static_cast<int64_t>(it.units) * a.H;
-      it = kv_item<kAtRows>(a, ++pair, tiles, bad);
-    }
-    h = static_cast<int>((u - at) / it.units);
-    ta = static_cast<int>(u - at - static_cast<int64_t>(h) * it.units);
-    tb = static_cast<int>(min(static_cast<int64_t>(it.units), ta + (u1 - u)));
-    e_tb = max(ta, min(tb, it.e_units));
-    u += tb - ta;
-    return true;
-  }
-};
-
 __global__ void __launch_bounds__(kAtThreads, 1)
 kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut* __restrict__ cuts) {
   extern __shared__ __align__(16) uint8_t asm_raw[];
@@ -270,19 +249,12 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
   if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
   int64_t mine0;
-  const int64_t U = kv_total_units<kAtRows, kAtThreads>(a, tiles, warp_sums, mine0);
+  const int64_t U = kv_total_cost<kAtRows, kAtItemCost, kAtThreads>(a, tiles, warp_sums, mine0);
   const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));
   if (static_cast<int>(blockIdx.x) >= ctas) return;  // before any barrier or tensor memory
-  AtWalk w;
-  w.u = w.u0 = kv_share(U, blockIdx.x, ctas);
-  w.u1 = kv_share(U, blockIdx.x + 1, ctas);
-  kv_find_unit<kAtRows, kAtThreads>(a, tiles, mine0, w.u0, found);
-  w.pair = static_cast<int>(found[0]);
-  w.at = found[1];
-  {
-    bool bad = false;
-    w.it = kv_item<kAtRows>(a, w.pair, tiles, bad);
-  }
+  kv_find<kAtRows, kAtItemCost, kAtThreads>(a, tiles, mine0, kv_share(U, blockIdx.x, ctas), found);
+  KvWalk<kAtRows, kAtItemCost> w;
+  w.begin(a, tiles, U, ctas, found);
 
   kv_check_codebook(a.codebook);
   for (int i = threadIdx.x; i < 64 * 32; i += kAtThreads)
@@ -330,12 +302,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       const int tr = it.row0 + (on ? r : 0), tok = tr / a.G, head = w.h * a.G + (tr - tok * a.G);
       const uint16_t* qrow = a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + head * kKvDim;
       const int lim = on ? it.p + tok + 1 : 0;
-      if (threadIdx.x == 0 && w.ta > 0 && w.u - (w.tb - w.ta) == w.u0) {
-        const int64_t s0 = w.at + static_cast<int64_t>(w.h) * it.units, s1 = s0 + it.units;
-        int count = 0;
-        if (kv_share(U, blockIdx.x - 1, ctas) <= s0)
-          count = 1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - blockIdx.x;
-        cuts[blockIdx.x] = {count, it.b, w.h, it.row0};
+      if (threadIdx.x == 0) {
+        KvCut cut;
+        if (w.note(a, U, ctas, cut)) cuts[blockIdx.x] = cut;
       }
       // m: the row's reference; lf: log2 of the power of two that keeps p n in
       // binary16's range, in l as in O; l: this thread's share of the row's sum
