@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kKvMaxRequests = 8192;  // prefix sums of all requests in shared memory
 constexpr int kTabThreads = 1024;
-constexpr int kAppThreads = 256;
+constexpr int kAppThreads = 128;
 
 // Encoded tokens among n (R slots of window).
 __host__ __device__ inline int64_t kv_enc(int64_t n, int64_t R) { return n > R ? n - R : 0; }
@@ -148,122 +148,276 @@ kv_tables_kernel(const int32_t* __restrict__ n_past, const int32_t* __restrict__
   if (full) raise_device_error(HLWQ_DEVERR_KV_PAGES);
 }
 
-// The request of token t: the last one that begins at or before t (requests
-// without tokens are passed over); -1 when t is behind the last token or the
-// offsets are not usable.
-__device__ __forceinline__ int kv_request_of(const int32_t* __restrict__ cu, int B, int64_t t) {
-  if (t >= __ldg(cu + B)) return -1;
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (__ldg(cu + m) <= t) lo = m;
-    else hi = m;
+// The request of token t < cu[B]: the last one that begins at or before t
+// (requests without tokens are passed over), found by the whole warp, 32
+// probes at a time.
+__device__ __forceinline__ int kv_request_of(const int32_t* __restrict__ cu, int B, int64_t t, int lane) {
+  int lo = 0, n = B;  // it is among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, i < n && __ldg(cu + lo + i) <= t);
+    const int k = le ? 31 - __clz(le) : 0;  // probe 0 counts as <= t
+    lo += k * step;
+    n = min(step, n - k * step);
   }
   return lo;
 }
 
-// Eight lanes per vector, four vectors per warp; vector v = (token t, head h,
-// key or value).  The vector's lanes read the token that leaves (from the ring
-// or, when the chunk is longer than the window, from the chunk), encode it, and
-// then write the ring slot's new content: slot (p + j) % R of new token j < R
-// ends up with the chunk's last token of that residue, so one group of lanes
-// reads and overwrites a slot and no other touches it.
-__global__ void __launch_bounds__(kAppThreads)
+// binary16 norm and codes of one vector in fp64, by the whole warp (lane: eight
+// values): the definition itself, for vectors that fp32 cannot decide.
+__device__ __noinline__ void kv_encode_exact(const uint16_t* src, const double* mid, uint8_t* dst, uint16_t* nrm_out,
+                                             int lane) {
+  const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * lane);
+  const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+  double v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = static_cast<double>(bf16x2_lo(wd[k]));
+    v[2 * k + 1] = static_cast<double>(bf16x2_hi(wd[k]));
+  }
+  double ss = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ss = fma(v[e], v[e], ss);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  const double nrm = sqrt(ss);
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & h) == 0) {
+        const double a = v[i], b = v[i + h];
+        v[i] = a + b;
+        v[i + h] = a - b;
+      }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double p = __shfl_xor_sync(0xffffffffu, v[i], o);
+      v[i] = (lane & o) ? p - v[i] : v[i] + p;
+    }
+  uint32_t bits = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double y = nrm > 0.0 ? v[e] / nrm : 0.0;
+    uint32_t code = 0u;
+    for (int k = 0; k < kKvLevels - 1; ++k) code += y > mid[k] ? 1u : 0u;
+    bits |= code << (3 * e);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) dst[3 * lane + k] = static_cast<uint8_t>(bits >> (8 * k));
+  if (lane == 0) *nrm_out = static_cast<uint16_t>(f16_rne_from_f64(nrm));
+}
+
+// Eight lanes per vector, four vectors per warp.  A token has 2 H vectors (head,
+// key or value); a warp takes four of them (all it has of two tokens when H = 1)
+// and goes through a contiguous range of tokens, so that requests and
+// ring slots are followed from one token to the next instead of being searched for.
+//
+// The vector's lanes read the token that leaves (from the ring or, when the
+// chunk is longer than the window, from the chunk), encode it, and then write
+// the ring slot's new content: slot (p + j) % R of new token j < R ends up with the
+// chunk's last token of that residue, so one group of lanes reads and overwrites
+// a slot and no other touches it.
+//
+// Bound: HBM by its bytes (512 read, 98 written per vector); in fact the
+// instructions of the rotation (8 butterfly stages) and of 256 decisions.  The
+// definition asks for fp64: y_j = (x H)_j / |x| against the midpoints, |x| to the
+// nearest binary16.  fp32 decides nearly always.  With u = 2^-24 and n = |x|:
+//   - a butterfly value is off by at most ((1 + u)^8 - 1) sum |x_i| <= 8.01 u 16 n;
+//   - the squares are exact, a path through their sum has 8 additions: n is off by
+//     less than 7 u n, a border mid n (|mid| < 3) by less than 9 u 3 n;
+// so a value farther than 156 u n < 2^-16 n from every border is decided, and a norm
+// farther than 2^-20 n from every binary16 rounding border.  About one vector in
+// a hundred is not, and is encoded by the whole warp in fp64 (kv_encode_exact).
+//
+// The decision uses the codebook's symmetry (mid[6 - k] = -mid[k], as Lloyd-Max
+// gives it): three borders for |v|; another codebook goes to fp64 throughout.
+__global__ void __launch_bounds__(kAppThreads, 4)
 kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __restrict__ V, int64_t ldv, int64_t T,
                  int H, const int64_t* __restrict__ slot_map, const int32_t* __restrict__ cu,
                  const int32_t* __restrict__ n_past, int B, const float* __restrict__ codebook,
                  uint8_t* __restrict__ kp, uint16_t* __restrict__ kn, uint8_t* __restrict__ vp,
-                 uint16_t* __restrict__ vn, int64_t num_slots, int64_t P, uint16_t* kwin, uint16_t* vwin, int64_t R) {
+                 uint16_t* __restrict__ vn, int64_t num_slots, int P, uint16_t* kwin, uint16_t* vwin, int R) {
   __shared__ double mid[kKvLevels - 1];
   kv_check_codebook(codebook);
   if (threadIdx.x < kKvLevels - 1)
     mid[threadIdx.x] = 0.5 * (static_cast<double>(__ldg(codebook + threadIdx.x)) +
                               static_cast<double>(__ldg(codebook + threadIdx.x + 1)));
   __syncthreads();
+  const bool plain = mid[3] == 0.0 && mid[4] == -mid[2] && mid[5] == -mid[1] && mid[6] == -mid[0] && mid[6] < 3.0;
+  const float b1 = static_cast<float>(mid[4]), b2 = static_cast<float>(mid[5]), b3 = static_cast<float>(mid[6]);
   const int lane = threadIdx.x & 31, l8 = lane & 7;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kAppThreads + threadIdx.x) >> 5;
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kAppThreads / 32);
-  const int64_t nvec = T * H * 2;
-  for (int64_t v0 = warp * 4; v0 < nvec; v0 += nwarps * 4) {
-    const int64_t vi = v0 + (lane >> 3);
-    const int64_t t = vi / (2 * H);
-    const int rem = static_cast<int>(vi - t * 2 * H), h = rem >> 1;
-    const bool is_v = rem & 1;
-    const uint16_t* X = is_v ? V : K;
-    const int64_t ldx = is_v ? ldv : ldk;
-    uint16_t* win = is_v ? vwin : kwin;
-    int b = -1;
-    int64_t c0 = 0, j = 0, p = 0, n = 0;
-    if (vi < nvec) {
-      b = kv_request_of(cu, B, t);
-      if (b >= 0) {
-        c0 = __ldg(cu + b);
-        n = __ldg(cu + b + 1) - c0;
-        j = t - c0;
-        p = __ldg(n_past + b);
-        if (c0 < 0 || j < 0 || j >= n || c0 + n > T || p < 0) {
-          raise_device_error(HLWQ_DEVERR_KV_RANGE);
-          b = -1;
-        }
+  const int64_t end = min(T, static_cast<int64_t>(__ldg(cu + B)));
+  if (__ldg(cu + B) > T && blockIdx.x == 0 && threadIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+  const int toks = H == 1 ? 2 : 1, groups = H == 1 ? 1 : (H + 1) / 2;  // tokens of a step, warps side by side
+  const int lanes = static_cast<int>(nwarps / groups);                 // warps along the tokens
+  const int group = static_cast<int>(warp % groups);
+  const int64_t each = ((end + lanes - 1) / lanes + toks - 1) / toks * toks;
+  const int64_t tb = warp / groups * each, te = min(end, tb + each);
+  if (warp / groups >= lanes || tb >= te) return;
+  const int rem = H == 1 ? (lane >> 3) & 1 : 4 * group + (lane >> 3), h = rem >> 1;
+  const bool is_v = rem & 1, has = rem < 2 * H;
+  const uint16_t* X = (is_v ? V : K) + (has ? h : 0) * kKvDim + 32 * l8;
+  const int64_t ldx = is_v ? ldv : ldk;
+  uint16_t* win = (is_v ? vwin : kwin) + 32 * l8;
+  int64_t t = tb + (H == 1 ? lane >> 4 : 0);  // this lane's token
+  int b = kv_request_of(cu, B, tb, lane);
+  int64_t next = -1;                          // the first token behind request b's
+  int c0 = 0, p = 0, n = 0, at = 0;           // its first token, lengths, ring slot of token t
+  bool live = false;
+  // one token ahead: whether a token leaves as it enters, from where (its values
+  // are requested at once) and to which slot; its own ring slot and what goes there
+  struct {
+    bool leaves, ring;
+    int64_t slot;
+    uint16_t* rs;
+    const uint16_t *src, *fresh;
+    uint4 u[4];
+  } a;
+  auto look = [&] {
+    a.leaves = false;
+    a.ring = false;
+    if (!has || t >= te) return;
+    if (t >= next) {  // another request
+      while (b + 1 < B && __ldg(cu + b + 1) <= t) ++b;
+      c0 = __ldg(cu + b);
+      next = __ldg(cu + b + 1);
+      p = __ldg(n_past + b);
+      live = c0 >= 0 && t >= c0 && t < next && next <= T && p >= 0;
+      if (!live) {
+        raise_device_error(HLWQ_DEVERR_KV_RANGE);
+        next = t + 1;
       }
+      n = static_cast<int>(next - c0);
+      at = R ? static_cast<int>((static_cast<uint32_t>(p) + static_cast<uint32_t>(t - c0)) % static_cast<uint32_t>(R)) : 0;
+    } else {
+      at += toks;
+      while (at >= R && R) at -= R;
     }
-    const int64_t i = p + j - R;  // the token that leaves
+    if (!live) return;
+    const int j = static_cast<int>(t - c0);
+    a.ring = j < R;  // this group owns a ring slot
+    a.rs = win + ((static_cast<int64_t>(b) * H + h) * R + at) * kKvDim;
+    a.src = a.ring ? a.rs : X + (t - R) * ldx;
+    a.fresh = X + (c0 + static_cast<int64_t>(n - j <= R || !a.ring ? j : j + (n - 1 - j) / R * R)) * ldx;
+    if (p >= R || j >= R - p) {  // token p + j - R leaves
+      a.leaves = true;
+      a.slot = __ldg(slot_map + t);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) a.u[c] = reinterpret_cast<const uint4*>(a.src)[c];
+    }
+  };
+  look();
+  for (int64_t step = tb; step < te; step += toks) {
+    const auto now = a;
     int64_t slot = -1;
-    if (b >= 0 && i >= 0) {
-      slot = __ldg(slot_map + t);
+    if (now.leaves) {
+      slot = now.slot;
       if (slot < 0 || slot >= num_slots) {
         raise_device_error(HLWQ_DEVERR_KV_RANGE);
         slot = -1;
       }
     }
-    const bool ring = b >= 0 && j < R;  // this group owns a ring slot
-    uint16_t* rs = win + ((static_cast<int64_t>(b) * H + h) * R + (ring ? (p + j) % R : 0)) * kKvDim + 32 * l8;
-    const uint4* src = slot < 0 ? nullptr
-                       : ring   ? reinterpret_cast<const uint4*>(rs)
-                                : reinterpret_cast<const uint4*>(X + (t - R) * ldx + h * kKvDim + 32 * l8);
-    double v[32];
+    t += toks;
+    look();  // (its ring slot, if it has one, is another one than this token's)
+    float2 v[16];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (src) u = src[c];
+      const uint4 u = slot >= 0 ? now.u[c] : make_uint4(0u, 0u, 0u, 0u);
       const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[8 * c + 2 * k] = static_cast<double>(bf16x2_lo(wd[k]));
-        v[8 * c + 2 * k + 1] = static_cast<double>(bf16x2_hi(wd[k]));
+      for (int k = 0; k < 4; ++k) v[4 * c + k] = make_float2(bf16x2_lo(wd[k]), bf16x2_hi(wd[k]));
+    }
+    if (__any_sync(0xffffffffu, slot >= 0)) {
+      // sum of squares: a tree of 5 + 3 additions
+      float2 sq[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sq[k] = add2(mul2(v[k], v[k]), mul2(v[k + 8], v[k + 8]));
+#pragma unroll
+      for (int o = 4; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < o; ++k) sq[k] = add2(sq[k], sq[k + o]);
+      const float ss = oct_sum(sq[0].x + sq[0].y);
+      // rotation: pairs within a register pair, then between pairs, then lanes
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = make_float2(v[k].x + v[k].y, v[k].x - v[k].y);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if ((k & o) == 0) {
+            const float2 x = v[k], y = v[k + o];
+            v[k] = add2(x, y);
+            v[k + o] = sub2(x, y);
+          }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        const float sg = (lane & o) ? -1.0f : 1.0f;
+        const float2 s2 = make_float2(sg, sg);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 x = make_float2(__shfl_xor_sync(0xffffffffu, v[k].x, o), __shfl_xor_sync(0xffffffffu, v[k].y, o));
+          v[k] = fma2(v[k], s2, x);  // +-v + x, one rounding
+        }
       }
+      const float nrm = sqrtf(ss);
+      const float t1 = b1 * nrm, t2 = b2 * nrm, t3 = b3 * nrm;
+      // |x| between borders m and m + 1: code 3.5 +- (m + 0.5); eight codes are
+      // added up in an fp32 word (24 bits, exact)
+      uint32_t q[4];
+      float near = INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float acc = 3.5f * 2396745.0f;  // 3.5 (8^8 - 1) / 7
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = (e & 1) ? v[4 * c + (e >> 1)].y : v[4 * c + (e >> 1)].x, ax = fabsf(x);
+          const bool p1 = ax > t2;
+          const float tb = p1 ? t3 : t1, d = ax - tb;
+          float mag = p1 ? 2.5f : 0.5f;
+          mag = d > 0.0f ? mag + 1.0f : mag;
+          near = fminf(fminf(near, ax), fminf(fabsf(ax - t2), fabsf(d)));
+          acc = fmaf(copysignf(mag, x), static_cast<float>(1 << (3 * e)), acc);
+        }
+        q[c] = static_cast<uint32_t>(acc);
+      }
+      near = fminf(near, __shfl_xor_sync(0xffffffffu, near, 1));
+      near = fminf(near, __shfl_xor_sync(0xffffffffu, near, 2));
+      near = fminf(near, __shfl_xor_sync(0xffffffffu, near, 4));
+      // the norm's rounding to binary16: both ends of its interval agree
+      const uint32_t h0 = __half_as_ushort(__float2half_rn(nrm * (1.0f - 0x1p-20f)));
+      const uint32_t h1 = __half_as_ushort(__float2half_rn(nrm * (1.0f + 0x1p-20f)));
+      const bool sure = plain && ss > 0x1p-100f && ss < 0x1p100f && near > nrm * 0x1p-16f && h0 == h1;
+      const int64_t page = slot >> 31 ? slot / P : static_cast<int64_t>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(P));
+      const int64_t row = page * H * P + static_cast<int64_t>(h) * P + (slot - page * P);
+      uint8_t* out = (is_v ? vp : kp) + row * kKvBytes;
+      uint16_t* out_n = (is_v ? vn : kn) + row;
+      if (slot >= 0 && sure) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(out + 12 * l8);
+        dst[0] = q[0] | (q[1] << 24);
+        dst[1] = (q[1] >> 8) | (q[2] << 16);
+        dst[2] = (q[2] >> 16) | (q[3] << 8);
+        if (l8 == 0) *out_n = static_cast<uint16_t>(h0);
+      }
+      uint32_t again = __ballot_sync(0xffffffffu, slot >= 0 && !sure && l8 == 0);
+      while (again) {
+        const int from = __ffs(static_cast<int>(again)) - 1;
+        again &= again - 1;
+        kv_encode_exact(reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(now.src), from)),
+                        mid,
+                        reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), from)),
+                        reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_n), from)),
+                        lane);
+      }
+      __syncwarp();  // the ring has been read by every lane
     }
-    if (ring) {
-      const int64_t jf = j + (n - 1 - j) / R * R;
-      const uint4* xs = reinterpret_cast<const uint4*>(X + (c0 + jf) * ldx + h * kKvDim + 32 * l8);
+    if (now.ring) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(rs)[c] = __ldg(xs + c);
-    }
-    if (!__any_sync(0xffffffffu, slot >= 0)) continue;
-    double ss = 0.0;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) ss = fma(v[e], v[e], ss);
-    ss = oct_sum(ss);
-    const double nrm = sqrt(ss);
-    kv_fwht(v, lane);
-    uint32_t w[3] = {0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const double y = nrm > 0.0 ? v[e] / nrm : 0.0;
-      uint32_t code = 0u;
-#pragma unroll
-      for (int k = 0; k < kKvLevels - 1; ++k) code += y > mid[k] ? 1u : 0u;
-      const int bit = 3 * e, k = bit >> 5, sh = bit & 31;
-      w[k] |= code << sh;
-      if (sh > 29) w[k + 1] |= code >> (32 - sh);
-    }
-    if (slot >= 0) {
-      const int64_t row = (slot / P * H + h) * P + slot % P;
-      uint32_t* dst = reinterpret_cast<uint32_t*>((is_v ? vp : kp) + row * kKvBytes + 12 * l8);
-      dst[0] = w[0];
-      dst[1] = w[1];
-      dst[2] = w[2];
-      if (l8 == 0) (is_v ? vn : kn)[row] = static_cast<uint16_t>(f16_rne_from_f64(nrm));
+      for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(now.rs)[c] = __ldg(reinterpret_cast<const uint4*>(now.fresh) + c);
     }
   }
 }
@@ -290,10 +444,14 @@ int launch_kv_append(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t 
                      const int64_t* slot_map, const int32_t* cu, const int32_t* n_past, int B, const float* codebook,
                      uint8_t* kp, uint16_t* kn, uint8_t* vp, uint16_t* vn, int64_t num_pages, int64_t P,
                      uint16_t* kwin, uint16_t* vwin, int64_t R, cudaStream_t stream) {
-  const int64_t max_ctas = static_cast<int64_t>(sm_count()) * 4;
-  const int grid = static_cast<int>(std::min<int64_t>(max_ctas, ceil_div(T * H * 2, kAppThreads / 8)));
+  // four CTAs per SM; a few tokens get a warp per step, and enough warps for every group of vectors
+  const int64_t groups = H == 1 ? 1 : (H + 1) / 2, warps = std::max<int64_t>(groups, T * groups);
+  const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(static_cast<int64_t>(sm_count()) * 4,
+                                                                        ceil_div(groups, kAppThreads / 32)),
+                                                      ceil_div(warps, kAppThreads / 32)));
   kv_append_kernel<<<grid, kAppThreads, 0, stream>>>(K, ldk, V, ldv, T, H, slot_map, cu, n_past, B, codebook, kp, kn, vp,
-                                                     vn, num_pages * P, P, kwin, vwin, R);
+                                                     vn, num_pages * P, static_cast<int>(P), kwin, vwin,
+                                                     static_cast<int>(R));
   return cudaGetLastError() == cudaSuccess ? HLWQ_OK : HLWQ_ECUDA;
 }
 

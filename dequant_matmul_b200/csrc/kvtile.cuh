@@ -335,8 +335,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float4 x = lds_f4(nb + 32 * i);
-            v[i][0] = fmul2(v[i][0], make_float2(x.x, x.y));
-            v[i][1] = fmul2(v[i][1], make_float2(x.z, x.w));
+            v[i][0] = mul2(v[i][0], make_float2(x.x, x.y));
+            v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
           }
         }
         const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + 520);  // 16-key groups whose page is there
@@ -412,8 +412,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float4 x = lds_f4(nb + 256 + 32 * i);
-            v[i][0] = fmul2(v[i][0], make_float2(x.x, x.y));
-            v[i][1] = fmul2(v[i][1], make_float2(x.z, x.w));
+            v[i][0] = mul2(v[i][0], make_float2(x.x, x.y));
+            v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
           }
           uint32_t x[16];
 #pragma unroll
