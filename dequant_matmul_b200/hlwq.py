@@ -368,68 +368,78 @@ class KVWindowCache:
         return S
 
 
-class _on:
-    """Makes a tensor's device the current one for a launch (a no-op when it
-    already is), so that the call and torch's current stream belong to it."""
-
-    def __init__(self, t: torch.Tensor, what: str, *others):
-        for o in others:
-            if o is not None and o.device != t.device:
-                raise HLWQError(f"{what}: tensors on {t.device} and {o.device}")
-        here = torch.cuda.current_device()
-        self.guard = None if t.device.index == here else torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _array(t: torch.Tensor, name: str, dtype, shape):
-    """A contiguous CUDA tensor of this type and shape (None: any size)."""
-    _cuda(t, name)
+# The calls of the paged cache take many small arrays and are short on the device,
+# so their checks are written to cost little: one comparison chain per tensor,
+# the message is put together only when it fails.
+def _refuse(t, name: str, dtype, shape, dev: int):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise HLWQError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise HLWQError(f"{name} is on cuda:{t.get_device()}, the call's other tensors on cuda:{dev}")
     if t.dtype != dtype:
         raise HLWQError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+    if tuple(t.shape) != tuple(shape):
         raise HLWQError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    raise HLWQError(f"{name} must be contiguous")
 
 
-def _heads(t: torch.Tensor, name: str):
-    """A bf16 CUDA tensor [T][heads][256] whose tokens are contiguous (any pitch
-    from token to token)."""
+def _array(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this type, shape and device."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise HLWQError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise HLWQError(f"{name} must be bfloat16, not {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != 256 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 256):
-        raise HLWQError(f"{name} must be [T][heads][256] with contiguous tokens")
+    return t.get_device()
 
 
-def _pitch(t: torch.Tensor) -> int:
-    """Elements from token to token (a single token's own length: its stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * 256
+def _heads(t: torch.Tensor, name: str, dev: int) -> int:
+    """The elements from token to token of a bf16 tensor [T][heads][256] whose
+    tokens are contiguous."""
+    if t.get_device() != dev or t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != 256:
+        if t.dim() != 3 or t.shape[2] != 256:
+            raise HLWQError(f"{name} must be [T][heads][256], not {list(t.shape)}")
+        _refuse(t, name, torch.bfloat16, t.shape, dev)
+    T, heads, _ = t.shape
+    pitch, of_head, of_value = t.stride()
+    if of_value != 1 or (heads > 1 and of_head != 256):
+        raise HLWQError(f"{name}: the heads of a token must be contiguous")
+    return pitch if T > 1 else heads * 256  # (the stride of a single token says nothing)
 
 
-def _pool(k_pages, v_pages, window, B: int):
-    """Checks the pages and windows of a paged cache; (num_pages, kv_heads, page_size, R)."""
+def _pool(k_pages, v_pages, window, B: int, dev: int):
+    """Checks a paged cache: (addresses of K's and V's codes and norms, of the
+    windows, num_pages, kv_heads, page_size, R)."""
     packed = k_pages[0]
     if packed.dim() != 4:
-        raise HLWQError("packed pages must be [num_pages][kv_heads][page_size][96]")
+        raise HLWQError(f"packed pages must be [num_pages][kv_heads][page_size][96], not {list(packed.shape)}")
     n, h, p, _ = packed.shape
-    for name, (pk, nr) in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _array(pk, f"{name} packed", torch.uint8, (n, h, p, 96))
-        _array(nr, f"{name} norms", torch.uint16, (n, h, p))
-    R = 0
-    if window is not None:
-        if window[0].dim() != 4:
-            raise HLWQError("windows must be [B][kv_heads][R][256]")
-        R = window[0].shape[2]
-        for name, w in (("k window", window[0]), ("v window", window[1])):
-            _array(w, name, torch.bfloat16, (B, h, R, 256))
-    return n, h, p, R
+    codes, norms = (n, h, p, 96), (n, h, p)
+    at = (_array(packed, "k_pages[0]", torch.uint8, codes, dev), _array(k_pages[1], "k_pages[1]", torch.uint16, norms, dev),
+          _array(v_pages[0], "v_pages[0]", torch.uint8, codes, dev),
+          _array(v_pages[1], "v_pages[1]", torch.uint16, norms, dev))
+    if window is None:
+        return at, None, None, n, h, p, 0
+    if window[0].dim() != 4:
+        raise HLWQError(f"windows must be [B][kv_heads][R][256], not {list(window[0].shape)}")
+    R = window[0].shape[2]
+    shape = (B, h, R, 256)
+    return (at, _array(window[0], "window[0]", torch.bfloat16, shape, dev),
+            _array(window[1], "window[1]", torch.bfloat16, shape, dev), n, h, p, R)
+
+
+def _launch(what: str, fn, dev: int, stream, *args):
+    """Calls a library function whose last argument is the stream, on the tensors'
+    device and (by default) its current stream."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(what, fn, dev, stream, *args)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if status != HLWQ_OK:
+        _check(status, what)
 
 
 def kv_block_tables(n_past, n_new, free_pages, n_free, block_table, page_size: int, R: int, T: int = None,
@@ -440,28 +450,27 @@ def kv_block_tables(n_past, n_new, free_pages, n_free, block_table, page_size: i
     T is the number of rows of the step's K, V and Q (given by slot_map, if
     that is passed).  Returns (cu_new int32 [B + 1], slot_map int64 [T],
     n_free_out int32 [1])."""
-    _array(n_past, "n_past", torch.int32, (None,))
-    B = n_past.shape[0]
-    _array(n_new, "n_new", torch.int32, (B,))
-    _array(free_pages, "free_pages", torch.int32, (None,))
-    _array(n_free, "n_free", torch.int32, (1,))
-    _array(block_table, "block_table", torch.int32, (B, None))
+    dev, i32 = _device_of(n_past, "n_past"), torch.int32
+    B = n_past.numel()
     if slot_map is None:
         if T is None:
             raise HLWQError("kv_block_tables needs T or slot_map")
         slot_map = torch.empty(T, dtype=torch.int64, device=n_past.device)
+    elif T is None:
+        T = slot_map.numel()
     if n_free_out is None:
-        n_free_out = torch.empty(1, dtype=torch.int32, device=n_past.device)
+        n_free_out = torch.empty(1, dtype=i32, device=n_past.device)
     if cu_new is None:
-        cu_new = torch.empty(B + 1, dtype=torch.int32, device=n_past.device)
-    _array(slot_map, "slot_map", torch.int64, (T,))
-    _array(n_free_out, "n_free_out", torch.int32, (1,))
-    _array(cu_new, "cu_new", torch.int32, (B + 1,))
-    with _on(n_past, "kv_block_tables", n_new, free_pages, n_free, n_free_out, block_table, cu_new, slot_map):
-        _check(lib.hlwq_kv_block_tables(_ptr(n_past), _ptr(n_new), B, R, page_size, _ptr(free_pages),
-                                        free_pages.shape[0], _ptr(n_free), _ptr(n_free_out), _ptr(block_table),
-                                        block_table.shape[1], _ptr(cu_new), _ptr(slot_map), slot_map.shape[0],
-                                        _stream(stream)), "hlwq_kv_block_tables")
+        cu_new = torch.empty(B + 1, dtype=i32, device=n_past.device)
+    cap = free_pages.numel()
+    if block_table.dim() != 2:
+        raise HLWQError(f"block_table must be [B][max_pages], not {list(block_table.shape)}")
+    width = block_table.shape[1]
+    _launch("hlwq_kv_block_tables", lib.hlwq_kv_block_tables, dev, stream, _array(n_past, "n_past", i32, (B,), dev),
+            _array(n_new, "n_new", i32, (B,), dev), B, R, page_size, _array(free_pages, "free_pages", i32, (cap,), dev),
+            cap, _array(n_free, "n_free", i32, (1,), dev), _array(n_free_out, "n_free_out", i32, (1,), dev),
+            _array(block_table, "block_table", i32, (B, width), dev), width,
+            _array(cu_new, "cu_new", i32, (B + 1,), dev), _array(slot_map, "slot_map", torch.int64, (T,), dev), T)
     return cu_new, slot_map, n_free_out
 
 
@@ -472,23 +481,17 @@ def kv_paged_append(K, V, slot_map, cu_new, n_past, k_pages, v_pages, window, cb
     window = (k, v) bf16 [B][kv_heads][R][256], or None (R = 0: every token is
     encoded); slot_map and cu_new as kv_block_tables gives them, n_past the
     lengths before the step."""
-    _heads(K, "K")
-    _heads(V, "V")
-    T, H = K.shape[0], K.shape[1]
-    _array(n_past, "n_past", torch.int32, (None,))
-    B = n_past.shape[0]
-    _array(cu_new, "cu_new", torch.int32, (B + 1,))
-    _array(slot_map, "slot_map", torch.int64, (T,))
-    _array(cb8, "cb8", torch.float32, (8,))
-    n, h, P, R = _pool(k_pages, v_pages, window, B)
+    dev = _device_of(K, "K")
+    ldk, ldv = _heads(K, "K", dev), _heads(V, "V", dev)
+    T, H, _ = K.shape
+    B = n_past.numel()
+    at, kw, vw, n, h, P, R = _pool(k_pages, v_pages, window, B, dev)
     if V.shape != K.shape or h != H:
         raise HLWQError(f"K {list(K.shape)}, V {list(V.shape)} and pages of {h} heads do not go together")
-    kw, vw = window if window is not None else (None, None)
-    with _on(K, "kv_paged_append", V, slot_map, cu_new, n_past, *k_pages, *v_pages, kw, vw, cb8):
-        _check(lib.hlwq_kv_paged_append(_ptr(K), _pitch(K), _ptr(V), _pitch(V), T, H, _ptr(slot_map), _ptr(cu_new),
-                                        _ptr(n_past), B, _ptr(cb8), _ptr(k_pages[0]), _ptr(k_pages[1]),
-                                        _ptr(v_pages[0]), _ptr(v_pages[1]), n, P, _ptr(kw), _ptr(vw), R,
-                                        _stream(stream)), "hlwq_kv_paged_append")
+    _launch("hlwq_kv_paged_append", lib.hlwq_kv_paged_append, dev, stream, K.data_ptr(), ldk, V.data_ptr(), ldv, T, H,
+            _array(slot_map, "slot_map", torch.int64, (T,), dev), _array(cu_new, "cu_new", torch.int32, (B + 1,), dev),
+            _array(n_past, "n_past", torch.int32, (B,), dev), B, _array(cb8, "cb8", torch.float32, (8,), dev), *at, n, P,
+            kw, vw, R)
 
 
 def kv_attention_workspace(Q, kv_heads: int, B: int, max_new: int) -> int:
@@ -502,33 +505,35 @@ def kv_paged_attention(Q, cu_new, n_past, block_table, k_pages, v_pages, window,
     of the step's new tokens over their requests' cached tokens and themselves,
     after kv_paged_append.  max_new bounds the new tokens of one request;
     scale defaults to 1 / 16.  Rows behind the last request's stay as they are."""
-    _heads(Q, "Q")
-    T, Hq = Q.shape[0], Q.shape[1]
-    _array(n_past, "n_past", torch.int32, (None,))
-    B = n_past.shape[0]
-    _array(cu_new, "cu_new", torch.int32, (B + 1,))
-    _array(block_table, "block_table", torch.int32, (B, None))
-    _array(cb8, "cb8", torch.float32, (8,))
-    n, H, P, R = _pool(k_pages, v_pages, window, B)
-    if Hq % H:
+    dev = _device_of(Q, "Q")
+    ldq = _heads(Q, "Q", dev)
+    T, Hq, _ = Q.shape
+    B = n_past.numel()
+    at, kw, vw, n, H, P, R = _pool(k_pages, v_pages, window, B, dev)
+    if H == 0 or Hq % H:
         raise HLWQError(f"{Hq} query heads are not a multiple of {H} kv heads")
     if out is None:
         out = torch.empty(T, Hq, 256, dtype=torch.bfloat16, device=Q.device)
-    _heads(out, "out")
-    if out.shape != Q.shape:
+    elif out.shape != Q.shape:
         raise HLWQError(f"out must be {list(Q.shape)}, not {list(out.shape)}")
-    kw, vw = window if window is not None else (None, None)
-    with _on(Q, "kv_paged_attention", cu_new, n_past, block_table, *k_pages, *v_pages, kw, vw, cb8, out, workspace):
-        if workspace is None:
+    if block_table.dim() != 2:
+        raise HLWQError(f"block_table must be [B][max_pages], not {list(block_table.shape)}")
+    width = block_table.shape[1]
+    if workspace is None:
+        if torch.cuda.current_device() != dev:
+            with torch.cuda.device(dev):
+                need = kv_attention_workspace(Q, H, B, max_new)
+        else:
             need = kv_attention_workspace(Q, H, B, max_new)
-            workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
-        _check(lib.hlwq_kv_paged_attention(_ptr(Q), _pitch(Q), T, Hq, H, 1.0 / 16.0 if scale is None else scale,
-                                           _ptr(cu_new), _ptr(n_past), B, max_new, _ptr(block_table),
-                                           block_table.shape[1], _ptr(cb8), _ptr(k_pages[0]), _ptr(k_pages[1]),
-                                           _ptr(v_pages[0]), _ptr(v_pages[1]), n, P, _ptr(kw), _ptr(vw), R, _ptr(out),
-                                           _pitch(out), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                           _stream(stream)), "hlwq_kv_paged_attention")
+        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise HLWQError(f"workspace must be contiguous and on cuda:{dev}")
+    _launch("hlwq_kv_paged_attention", lib.hlwq_kv_paged_attention, dev, stream, Q.data_ptr(), ldq, T, Hq, H,
+            0.0625 if scale is None else scale, _array(cu_new, "cu_new", torch.int32, (B + 1,), dev),
+            _array(n_past, "n_past", torch.int32, (B,), dev), B, max_new,
+            _array(block_table, "block_table", torch.int32, (B, width), dev), width,
+            _array(cb8, "cb8", torch.float32, (8,), dev), *at, n, P, kw, vw, R, out.data_ptr(), _heads(out, "out", dev),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
