@@ -21,125 +21,124 @@ constexpr int kKvMaxRequests = 8192;  // prefix sums of all requests in shared m
 constexpr int kTabThreads = 1024;
 constexpr int kAppThreads = 128;
 
-// Encoded tokens among n (R slots of window).
-__host__ __device__ inline int64_t kv_enc(int64_t n, int64_t R) { return n > R ? n - R : 0; }
+// Pages of the encoded tokens among n (R slots of window, P tokens to a page).
+__device__ __forceinline__ uint32_t kv_pages(uint32_t n, uint32_t R, uint32_t P) { return n > R ? (n - R + P - 1) / P : 0u; }
 
-// One request's lengths, checked: negative ones count as 0.
-__device__ __forceinline__ int kv_len(int v, bool& bad) {
-  if (v < 0) bad = true;
-  return v < 0 ? 0 : v;
-}
+constexpr uint32_t kTabCap = 0x3fffffffu;  // sums saturate here: two of them still add in 32 bits
 
 // Exclusive prefix sums over the CTA of two values per thread (kTabThreads
-// threads), and their totals.
-__device__ __forceinline__ void tab_scan(int64_t& a, int64_t& b, int64_t& ta, int64_t& tb, int64_t (*sums)[2]) {
+// threads, sums saturating at kTabCap), and their totals.
+__device__ __forceinline__ void tab_scan(uint32_t& a, uint32_t& b, uint32_t& ta, uint32_t& tb, uint2* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t a0 = a, b0 = b;
+  uint32_t ia = a, ib = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) a += x, b += y;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) ia = min(ia + x, kTabCap), ib = min(ib + y, kTabCap);
   }
-  if (lane == 31) sums[warp][0] = a, sums[warp][1] = b;
+  if (lane == 31) sums[warp] = make_uint2(ia, ib);
+  uint32_t ea = __shfl_up_sync(0xffffffffu, ia, 1), eb = __shfl_up_sync(0xffffffffu, ib, 1);
+  if (lane == 0) ea = eb = 0u;
   __syncthreads();
-  int64_t x = sums[lane][0], y = sums[lane][1];  // 32 warps: every warp scans their sums
+  uint32_t x = sums[lane].x, y = sums[lane].y;  // 32 warps: every warp scans their sums
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) x += u, y += v;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) x = min(x + u, kTabCap), y = min(y + v, kTabCap);
   }
   ta = __shfl_sync(0xffffffffu, x, 31);
   tb = __shfl_sync(0xffffffffu, y, 31);
-  const int64_t px = __shfl_sync(0xffffffffu, x, (warp + 31) & 31), py = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
-  a += (warp ? px : 0) - a0;
-  b += (warp ? py : 0) - b0;
+  const uint32_t px = __shfl_sync(0xffffffffu, x, (warp + 31) & 31), py = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+  a = min(ea + (warp ? px : 0u), kTabCap);
+  b = min(eb + (warp ? py : 0u), kTabCap);
   __syncthreads();
 }
 
+// The last i in [0, n) with v[i] <= x (v[0] <= x, ascending).
+__device__ __forceinline__ int tab_last(const uint32_t* v, int n, uint32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (v[m] <= x) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
+
 // Every CTA scans all requests (B <= 8192: a few KB from L2) and keeps
-// cu[b] (new tokens before request b) and first[b] (pages allocated before b)
-// in shared memory; then the CTAs share the work: requests round-robin, a warp
-// each, for the new table entries, and T in strides for the slot map.  A slot's
-// page is read from the table where the table had it before this call, and
-// from the free stack otherwise, so no CTA reads what another one writes.
+// cu[b] (new tokens before request b) and first[b] (pages taken before b) in shared
+// memory; then the CTAs share the new pages and the T slots in strides, each
+// finding its request by bisection.  A slot's page is read from the table where
+// the table had it before this call, and from the free stack otherwise, so no
+// CTA reads what another one writes and one launch does it all.  Bound by
+// latency: a decode step of 8 requests takes 4 us, one of 512 5 us, 139 thousand
+// slots of 32 prompts 4 us (launch included).
 __global__ void __launch_bounds__(kTabThreads)
-kv_tables_kernel(const int32_t* __restrict__ n_past, const int32_t* __restrict__ n_new, int B, int64_t R, int64_t P,
+kv_tables_kernel(const int32_t* __restrict__ n_past, const int32_t* __restrict__ n_new, int B, uint32_t R, uint32_t P,
                  const int32_t* __restrict__ free_pages, int64_t free_cap, const int32_t* __restrict__ n_free,
-                 int32_t* __restrict__ n_free_out, int32_t* __restrict__ table, int64_t max_pages,
-                 int32_t* __restrict__ cu_new, int64_t* __restrict__ slot_map, int64_t T) {
-  extern __shared__ __align__(16) int32_t tsm[];
-  int32_t* cu = tsm;                // [B + 1]
-  int32_t* first = tsm + B + 1;     // [B]
-  __shared__ int64_t sums[32][2];
-  bool bad = false, full = false;
-  int64_t ca = 0, cb = 0;
+                 int32_t* __restrict__ n_free_out, int32_t* __restrict__ table, uint32_t max_pages,
+                 int32_t* __restrict__ cu_new, int64_t* __restrict__ slot_map, uint32_t T) {
+  extern __shared__ __align__(16) uint32_t tsm[];
+  uint32_t* cu = tsm;             // [B + 1]
+  uint32_t* first = tsm + B + 1;  // [B + 1]
+  __shared__ uint2 sums[32];
+  const int have0 = __ldg(n_free);
+  bool bad = have0 < 0 || have0 > free_cap, full = false;
+  const int64_t have = have0 < 0 ? 0 : min(static_cast<int64_t>(have0), free_cap);
+  uint32_t ca = 0, cb = 0;
   for (int b0 = 0; b0 < B; b0 += kTabThreads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    int64_t n = 0, need = 0;
-    if (b < B) {
-      const int64_t p = kv_len(__ldg(n_past + b), bad);
-      n = kv_len(__ldg(n_new + b), bad);
-      const int64_t old = ceil_div(kv_enc(p, R), P), want = ceil_div(kv_enc(p + n, R), P);
-      if (want > max_pages) full = true;
+    uint32_t n = 0, need = 0;
+    if (b < B) {  // negative lengths count as 0
+      const int p = __ldg(n_past + b), m = __ldg(n_new + b);
+      bad |= p < 0 || m < 0;
+      const uint32_t up = max(p, 0), un = max(m, 0);
+      const uint32_t old = kv_pages(up, R, P), want = kv_pages(up + un, R, P);
+      full |= want > max_pages;
       need = min(want, max_pages) - min(old, max_pages);
+      n = min(un, kTabCap);
     }
-    int64_t a = n, c = need, ta, tb;
-    tab_scan(a, c, ta, tb, sums);
+    uint32_t ta, tb;
+    tab_scan(n, need, ta, tb, sums);
     if (b < B) {
-      cu[b] = static_cast<int32_t>(min(ca + a, static_cast<int64_t>(INT32_MAX)));
-      first[b] = static_cast<int32_t>(min(cb + c, static_cast<int64_t>(INT32_MAX)));
+      cu[b] = min(ca + n, kTabCap);
+      first[b] = min(cb + need, kTabCap);
     }
-    ca += ta;
-    cb += tb;
+    ca = min(ca + ta, kTabCap);
+    cb = min(cb + tb, kTabCap);
   }
-  int64_t have = __ldg(n_free);
-  if (have < 0 || have > free_cap) {
-    bad = true;
-    have = have < 0 ? 0 : free_cap;
-  }
-  if (ca > T) bad = true;
+  bad |= ca > T;
+  full |= cb > have;
   if (threadIdx.x == 0) {
-    cu[B] = static_cast<int32_t>(min(ca, static_cast<int64_t>(INT32_MAX)));
-    if (blockIdx.x == 0) {
-      if (cb > have) full = true;
-      *n_free_out = static_cast<int32_t>(cb > have ? 0 : have - cb);
-    }
+    cu[B] = ca;
+    first[B] = cb;
+    if (blockIdx.x == 0) *n_free_out = static_cast<int32_t>(cb > have ? 0 : have - cb);
   }
   __syncthreads();
   if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= B; b += kTabThreads) cu_new[b] = cu[b];
+    for (int b = threadIdx.x; b <= B; b += kTabThreads) cu_new[b] = static_cast<int32_t>(cu[b]);
 
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int b = blockIdx.x * (kTabThreads / 32) + warp; b < B; b += gridDim.x * (kTabThreads / 32)) {
-    bool x = false;
-    const int64_t p = kv_len(__ldg(n_past + b), x), n = cu[b + 1] - cu[b];
-    const int64_t old = min(ceil_div(kv_enc(p, R), P), max_pages), want = min(ceil_div(kv_enc(p + n, R), P), max_pages);
-    for (int64_t k = old + lane; k < want; k += 32) {
-      const int64_t at = have - 1 - (first[b] + k - old);
-      table[b * max_pages + k] = at >= 0 ? __ldg(free_pages + at) : -1;
-    }
+  const uint32_t me = blockIdx.x * kTabThreads + threadIdx.x, all = gridDim.x * kTabThreads;
+  for (uint32_t q = me; q < cb; q += all) {  // page q of this call
+    const int b = tab_last(first, B, q);
+    const uint32_t k = min(kv_pages(max(__ldg(n_past + b), 0), R, P), max_pages) + (q - first[b]);
+    if (k < max_pages)  // (always, below the sums' cap)
+      table[static_cast<int64_t>(b) * max_pages + k] = q < have ? __ldg(free_pages + (have - 1 - q)) : -1;
   }
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTabThreads + threadIdx.x; t < T;
-       t += static_cast<int64_t>(gridDim.x) * kTabThreads) {
+  for (uint32_t t = me; t < T; t += all) {
     int64_t slot = -1;
-    if (t < cu[B]) {
-      int lo = 0, hi = B;  // the last request that begins at or before t
-      while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (cu[m] <= t) lo = m;
-        else hi = m;
-      }
-      bool x = false;
-      const int64_t p = kv_len(__ldg(n_past + lo), x), i = p + (t - cu[lo]) - R;
-      if (i >= 0) {
-        const int64_t k = i / P, old = min(ceil_div(kv_enc(p, R), P), max_pages);
-        int64_t page = -1;
-        if (k < old) page = table[lo * max_pages + k];
+    if (t < ca) {
+      const int b = tab_last(cu, B, t);
+      const uint32_t p = max(__ldg(n_past + b), 0), in = p + (t - cu[b]);
+      if (in >= R) {  // token in - R leaves
+        const uint32_t i = in - R, k = i / P, old = min(kv_pages(p, R, P), max_pages);
+        int page = -1;
+        if (k < old) page = table[static_cast<int64_t>(b) * max_pages + k];
         else if (k < max_pages) {
-          const int64_t at = have - 1 - (first[lo] + k - old);
-          if (at >= 0) page = __ldg(free_pages + at);
+          const int64_t q = static_cast<int64_t>(first[b]) + (k - old);
+          if (q < have) page = __ldg(free_pages + (have - 1 - q));
         }
-        if (page >= 0) slot = page * P + i % P;
+        if (page >= 0) slot = static_cast<int64_t>(page) * P + (i - k * P);
       }
     }
     slot_map[t] = slot;
@@ -431,12 +430,13 @@ int launch_kv_tables(const int32_t* n_past, const int32_t* n_new, int B, int64_t
   static PerDeviceOnce attr;
   if (const int st = attr([&] {
         return cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (2 * kKvMaxRequests + 1) * 4) == cudaSuccess;
+                                    (2 * kKvMaxRequests + 2) * 4) == cudaSuccess;
       }))
     return st;
-  const int grid = static_cast<int>(std::min<int64_t>(sm_count(), std::max<int64_t>(1, ceil_div(T, kTabThreads))));
-  kv_tables_kernel<<<grid, kTabThreads, (2 * B + 1) * 4, stream>>>(n_past, n_new, B, R, P, free_pages, free_cap, n_free,
-                                                                   n_free_out, table, max_pages, cu_new, slot_map, T);
+  const int grid = static_cast<int>(std::min<int64_t>(sm_count(), ceil_div(T, kTabThreads)));
+  kv_tables_kernel<<<grid, kTabThreads, (2 * B + 2) * 4, stream>>>(
+      n_past, n_new, B, static_cast<uint32_t>(R), static_cast<uint32_t>(P), free_pages, free_cap, n_free, n_free_out, table,
+      static_cast<uint32_t>(max_pages), cu_new, slot_map, static_cast<uint32_t>(T));
   return cudaGetLastError() == cudaSuccess ? HLWQ_OK : HLWQ_ECUDA;
 }
 
