@@ -292,6 +292,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ float lds_half(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+  return half_bits_to_float(v);
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -381,8 +387,9 @@ __device__ __forceinline__ void rows_pv(float (&o)[NT][16][4], const uint32_t (&
       uint32_t a[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // a0, a1: even and odd dim of the first key pair; a2, a3 of the second
+        // one right shift serves two fields (the lower one is a multiplication further)
         const uint32_t v = pr[k >> 1][k & 1];
-        const uint32_t i = f == 0 ? v << 7 : f == 1 ? v << 1 : v >> (6 * f - 7);
+        const uint32_t i = f == 0 ? v * 128u : f == 1 ? (v >> 5) * 64u : f == 2 ? v >> 5 : f == 3 ? (v >> 17) * 64u : v >> 17;
         a[k] = lds32((i & 0x1f80u) | tab);
       }
 #pragma unroll
@@ -476,152 +483,195 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         for (int i = 0; i < 16; ++i) o[nt][i][k] = o[nt][i][2 + k] = 0.0f;
       }
 
-    // scores of 16 keys, times their factors k0 (this lane's first key, index `key`) and
-    // k1 (8 further); keys from `end` on are not there; the rows' references follow
-    auto score = [&](float (&d)[NT][4], float k0, float k1, int key, int end) {
+    // scores of M tiles of 16 keys, times their factors f[.][0] (this lane's first
+    // key, index key[.]) and f[.][1] (8 further); keys from end[.] on are not there.
+    // The rows' references follow; d becomes p = exp2(s - reference), up to 2^8
+    auto score = [&](auto& d, const auto& f, const auto& key, const auto& end) {
+      constexpr int M = sizeof(key) / sizeof(key[0]);
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int see = min(lim[nt][k], end);
-          d[nt][k] = key < see ? d[nt][k] * (k0 * qm[nt][k]) : -INFINITY;
-          d[nt][2 + k] = key + 8 < see ? d[nt][2 + k] * (k1 * qm[nt][k]) : -INFINITY;
-          over |= fmaxf(d[nt][k], d[nt][2 + k]) > m[nt][k] + 8.0f;
+          float x = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < M; ++i) {
+            const int see = min(lim[nt][k], end[i]);
+            d[i][nt][k] = key[i] < see ? d[i][nt][k] * (f[i][0] * qm[nt][k]) : -INFINITY;
+            d[i][nt][2 + k] = key[i] + 8 < see ? d[i][nt][2 + k] * (f[i][1] * qm[nt][k]) : -INFINITY;
+            x = fmaxf(x, fmaxf(d[i][nt][k], d[i][nt][2 + k]));
+          }
+          over |= x > m[nt][k] + 8.0f;
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float x = fmaxf(fmaxf(d[nt][k], d[nt][2 + k]), m[nt][k]);
+            float x = m[nt][k];
+#pragma unroll
+            for (int i = 0; i < M; ++i) x = fmaxf(x, fmaxf(d[i][nt][k], d[i][nt][2 + k]));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float f = ex2(m[nt][k] - x);
+            const float c = ex2(m[nt][k] - x);
             m[nt][k] = x;
-            l[nt][k] *= f;
+            l[nt][k] *= c;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              o[nt][i][k] *= f;
-              o[nt][i][2 + k] *= f;
+              o[nt][i][k] *= c;
+              o[nt][i][2 + k] *= c;
             }
           }
       }
-      // p = exp2(s - reference), up to 2^8, and the row sums
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[nt][k] = ex2(d[nt][k] - m[nt][k & 1]);
-        l[nt][0] += d[nt][0] + d[nt][2];
-        l[nt][1] += d[nt][1] + d[nt][3];
-      }
+        for (int i = 0; i < M; ++i) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[i][nt][k] = ex2(d[i][nt][k] - m[nt][k & 1]);
+          l[nt][0] += d[i][nt][0] + d[i][nt][2];
+          l[nt][1] += d[i][nt][1] + d[i][nt][3];
+        }
     };
 
-    // ---- encoded keys: tiles of 16, one warp each, kStages - 1 of them under way
+    // ---- encoded keys: each warp a contiguous part of the segment's tiles of 16,
+    // two tiles per step, the next step's two under way meanwhile
     const int e_tb = w.e_tb;
-    const int k_end = min(e_tb * kUnit, it.e_lim);
-    const int k_first = ta * kUnit + 16 * warp;
-    auto request = [&](int k0, int stage) {  // false: the page is not there
-      bool there = false;
-      if (k0 < k_end) {
-        const int kp = k0 / page_size;
-        const int page = kp < a.max_pages ? __ldg(a.table + it.b * a.max_pages + kp) : -1;
-        if (page < 0 || page >= a.num_pages) {
-          if (lane == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
-        } else {
-          there = true;
-          const int64_t row = (static_cast<int64_t>(page) * a.H + h) * a.P + (k0 - kp * page_size);
-          const uint32_t dst = wbuf + stage * kStage;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            cp_async16(dst + 16 * (lane + 32 * i), a.kp + row * kKvBytes + 16 * (lane + 32 * i));
-            cp_async16(dst + 1536 + 16 * (lane + 32 * i), a.vp + row * kKvBytes + 16 * (lane + 32 * i));
-          }
-          if (lane < 8) cp_async4(dst + 3072 + 4 * lane, a.kn + row + 2 * lane);
-          else if (lane < 16) cp_async4(dst + 3072 + 4 * lane, a.vn + row + 2 * (lane - 8));
-        }
-      }
-      cp_async_commit();
-      return there;
-    };
     if (ta < e_tb) {
-      uint32_t there = 0;  // bit i: the tile in stage i may be read
+      const int s_end = min(e_tb * kUnit, it.e_lim), n16 = (s_end - ta * kUnit + 15) >> 4;
+      const int k_first = ta * kUnit + 16 * (n16 * warp / kRowWarps);
+      const int k_end = min(s_end, ta * kUnit + 16 * (n16 * (warp + 1) / kRowWarps));
+      // the page that the next tile to be requested lies in, the one after it, tiles left in it
+      const int32_t* tab_row = a.table + it.b * a.max_pages;
+      int kp = k_first / page_size, left = (page_size - (k_first - kp * page_size)) >> 4;
+      int page = k_first < k_end && kp < a.max_pages ? __ldg(tab_row + kp) : -1;
+      int page2 = k_first + 16 * left < k_end && kp + 1 < a.max_pages ? __ldg(tab_row + kp + 1) : -1;
+      int64_t row = (static_cast<int64_t>(page) * a.H + h) * page_size + (k_first - kp * page_size);
+      int k_ask = k_first;
+      auto request = [&](uint32_t dst) -> uint32_t {  // two tiles; bit i: tile i's page is there
+        uint32_t there = 0;
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) there |= static_cast<uint32_t>(request(k_first + 64 * i, i)) << i;
-      int stage = 0;
-      for (int k0 = k_first; k0 < k_end; k0 += 64) {
-        const int ns = (stage + kStages - 1) % kStages;
-        __syncwarp();  // the stage is refilled: every lane has read it
-        there = (there & ~(1u << ns)) | static_cast<uint32_t>(request(k0 + 64 * (kStages - 1), ns)) << ns;
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        if ((there >> stage) & 1u) {
-          const uint32_t st = wbuf + stage * kStage;
-          const uint32_t nkw = lds32(st + 3072 + 4 * (g >> 1)), nkw2 = lds32(st + 3088 + 4 * (g >> 1));
-          const uint32_t nvw = lds32(st + 3104 + 4 * (g >> 1)), nvw2 = lds32(st + 3120 + 4 * (g >> 1));
-          const int ns16 = (g & 1) * 16;
-          uint32_t w0[6], w1[6];
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const uint2 x = lds64(st + g * kKvBytes + 24 * t4 + 8 * i), y = lds64(st + (g + 8) * kKvBytes + 24 * t4 + 8 * i);
-            w0[2 * i] = x.x, w0[2 * i + 1] = x.y;
-            w1[2 * i] = y.x, w1[2 * i + 1] = y.y;
+        for (int i = 0; i < 2; ++i, dst += kStage, k_ask += 16) {
+          if (k_ask >= k_end) continue;
+          if (left == 0) {
+            page = page2;
+            ++kp;
+            left = page_size >> 4;
+            row = (static_cast<int64_t>(page) * a.H + h) * page_size;
+            page2 = k_ask + page_size < k_end && kp + 1 < a.max_pages ? __ldg(tab_row + kp + 1) : -1;
           }
-          float d[2][NT][4];
+          --left;
+          if (page < 0 || page >= a.num_pages) {
+            if (lane == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+          } else {
+            there |= 1u << i;
+            const uint8_t* ks = a.kp + row * kKvBytes + 16 * lane;
+            const uint8_t* vs = a.vp + row * kKvBytes + 16 * lane;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < 3; ++c) {
+              cp_async16(dst + 16 * lane + 512 * c, ks + 512 * c);
+              cp_async16(dst + 1536 + 16 * lane + 512 * c, vs + 512 * c);
+            }
+            if (lane < 16) cp_async4(dst + 3072 + 4 * lane, (lane < 8 ? a.kn : a.vn) + row + 2 * (lane & 7));
+          }
+          row += 16;
+        }
+        cp_async_commit();
+        return there;
+      };
+      // row r of a tile's matrix operands is key r ^ (r >> 2 & 1): both operands are then
+      // read from the tile's 96-byte rows without bank conflicts
+      const int key_g = g ^ (g >> 2);
+      uint32_t there = request(wbuf), stage = 0;
+      for (int k0 = k_first; k0 < k_end; k0 += 32) {
+        __syncwarp();  // every lane has read the stage that is refilled
+        const uint32_t there2 = request(wbuf + (stage ^ 1u) * 2 * kStage);
+        cp_async_wait<1>();
+        __syncwarp();
+        const uint32_t st = wbuf + stage * 2 * kStage;
+        float d[2][NT][4], nk[2][2], nv[2][2];
+        const int key[2] = {k0 + key_g, k0 + 16 + key_g};
+        const int end[2] = {there & 1u ? k_end : 0, there & 2u ? k_end : 0};
+        {
+          uint32_t x[2][2][6];  // [tile][key g, g + 8]: 64 codes
 #pragma unroll
-            for (int k = 0; k < 4; ++k) d[0][nt][k] = d[1][nt][k] = 0.0f;
-#pragma unroll
-          for (int s = 0; s < 16; ++s) {
-            uint32_t af[4];
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int bit = 12 * s + 6 * k, wi = bit >> 5, sh = bit & 31;
-              uint32_t x, y;
-              if (sh > 26) x = __funnelshift_r(w0[wi], w0[wi + 1], sh - 7), y = __funnelshift_r(w1[wi], w1[wi + 1], sh - 7);
-              else if (sh >= 7) x = w0[wi] >> (sh - 7), y = w1[wi] >> (sh - 7);
-              else x = w0[wi] << (7 - sh), y = w1[wi] << (7 - sh);
-              af[2 * k] = lds32((x & 0x1f80u) | tab);
-              af[2 * k + 1] = lds32((y & 0x1f80u) | tab);
+              const uint32_t src = st + i * kStage + (key_g + 8 * k) * kKvBytes + 24 * t4;
+#pragma unroll
+              for (int c = 0; c < 3; ++c) {
+                const uint2 y = lds64(src + 8 * c);
+                x[i][k][2 * c] = y.x, x[i][k][2 * c + 1] = y.y;
+              }
+              const uint32_t n = st + i * kStage + 3072 + 2 * (key_g + 8 * k);
+              nk[i][k] = lds_half(n);
+              nv[i][k] = lds_half(n + 32);
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q = lds64(qfrag + ((nt * 16 + s) * 32 + lane) * 8);
-              mma_16816(d[s & 1][nt], af[0], af[1], af[2], af[3], q.x, q.y);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) d[0][nt][k] += d[1][nt][k];
-          uint32_t b[NT][2];
-          score(d[0], half_bits_to_float(static_cast<uint16_t>(nkw >> ns16)),
-                half_bits_to_float(static_cast<uint16_t>(nkw2 >> ns16)), k0 + g, k_end);
-          const float nv0 = half_bits_to_float(static_cast<uint16_t>(nvw >> ns16));
-          const float nv1 = half_bits_to_float(static_cast<uint16_t>(nvw2 >> ns16));
-          if (__any_sync(0xffffffffu, (k0 + g < k_end && nv0 * fv > 128.0f) || (k0 + g + 8 < k_end && nv1 * fv > 128.0f))) {
-            float x = fmaxf(k0 + g < k_end ? nv0 : 0.0f, k0 + g + 8 < k_end ? nv1 : 0.0f);
-#pragma unroll
-            for (int s = 4; s < 32; s <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
-            const int e = min(144, static_cast<int>(__float_as_uint(x) >> 23) + 1);  // x < 2^(e - 127)
-            const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23), f = nf / fv;  // x nf in [16, 32)
-            fv = nf;
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
+              for (int k = 0; k < 4; ++k) d[i][nt][k] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
+          for (int s = 0; s < 16; ++s) {
+            uint2 q[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) q[nt] = lds64(qfrag + ((nt * 16 + s) * 32 + lane) * 8);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t af[4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                // codes 4 s .. + 3: the second pair's index at bit 7, the first one's at bit 1
+                const int bit = 12 * s - 1, wi = bit >> 5, sh = bit & 31;
+                const uint32_t y = s == 0           ? x[i][k][0] * 2u
+                                   : sh + 12 <= 31 || wi == 5 ? x[i][k][wi] >> sh
+                                                    : __funnelshift_r(x[i][k][wi], x[i][k][wi + 1], sh);
+                af[k] = lds32(((y * 64u) & 0x1f80u) | tab);
+                af[2 + k] = lds32((y & 0x1f80u) | tab);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816(d[i][nt], af[0], af[1], af[2], af[3], q[nt].x, q[nt].y);
+            }
           }
-          const float f0 = nv0 * fv, f1 = nv1 * fv;
+        }
+        score(d, nk, key, end);
+        bool high = false;
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float x = key[i] + 8 * k < end[i] ? nv[i][k] : 0.0f;
+            high |= x * fv > 128.0f;
+            top = fmaxf(top, x);
+          }
+        if (__any_sync(0xffffffffu, high)) {
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+          const int e = min(144, static_cast<int>(__float_as_uint(top) >> 23) + 1);  // top < 2^(e - 127)
+          const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23), f = nf / fv;  // top nf in [16, 32)
+          fv = nf;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t b[NT][2];
+          const float f0 = nv[i][0] * fv, f1 = nv[i][1] * fv;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             // a key that is masked out has no say, whatever its norm is (NaN stays NaN)
             float p[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = d[0][nt][k] == 0.0f ? 0.0f : d[0][nt][k] * (k < 2 ? f0 : f1);
+            for (int k = 0; k < 4; ++k) p[k] = d[i][nt][k] == 0.0f ? 0.0f : d[i][nt][k] * (k < 2 ? f0 : f1);
             b[nt][0] = transpose_8x8(pack_half2(p[0], p[1]));
             b[nt][1] = transpose_8x8(pack_half2(p[2], p[3]));
           }
@@ -629,11 +679,12 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-              vw[k][i] = lds32(st + 1536 + (2 * t4 + (k & 1) + 8 * (k >> 1)) * kKvBytes + 12 * g + 4 * i);
+            for (int c = 0; c < 3; ++c)
+              vw[k][c] = lds32(st + i * kStage + 1536 + (((2 * t4 + (k & 1)) ^ (t4 >> 1)) + 8 * (k >> 1)) * kKvBytes + 12 * g + 4 * c);
           rows_pv<NT>(o, vw, tab, b);
         }
-        stage = (stage + 1) % kStages;
+        there = there2;
+        stage ^= 1u;
       }
       cp_async_wait<0>();
       __syncwarp();
@@ -674,9 +725,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {
       const int R = static_cast<int>(a.R);
       const int64_t ring = (static_cast<int64_t>(it.b) * a.H + h) * R;
-      float d[NT][4];
+      float d[1][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.0f;
+      for (int nt = 0; nt < NT; ++nt) d[0][nt][0] = d[0][nt][1] = d[0][nt][2] = d[0][nt][3] = 0.0f;
       {
         const bool on0 = k0 + g < w_end, on1 = k0 + g + 8 < w_end;
         const uint16_t* s0 = a.kwin + (ring + (on0 ? (k0 + g) % R : 0)) * kKvDim + 64 * t4;
@@ -690,20 +741,22 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 q0 = lds64(qfrag + C::kQFrag + ((nt * 16 + 2 * s) * 32 + lane) * 8);
             const uint2 q1 = lds64(qfrag + C::kQFrag + ((nt * 16 + 2 * s + 1) * 32 + lane) * 8);
-            mma_16816_bf16(d[nt], x.x, y.x, x.y, y.y, q0.x, q0.y);
-            mma_16816_bf16(d[nt], x.z, y.z, x.w, y.w, q1.x, q1.y);
+            mma_16816_bf16(d[0][nt], x.x, y.x, x.y, y.y, q0.x, q0.y);
+            mma_16816_bf16(d[0][nt], x.z, y.z, x.w, y.w, q1.x, q1.y);
           }
         }
       }
-      score(d, 1.0f, 1.0f, k0 + g, w_end);
+      const float one[1][2] = {{1.0f, 1.0f}};
+      const int key[1] = {k0 + g}, end[1] = {w_end};
+      score(d, one, key, end);
       uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t hi = pack_bf162(d[nt][2 * k], d[nt][2 * k + 1]);
+          const uint32_t hi = pack_bf162(d[0][nt][2 * k], d[0][nt][2 * k + 1]);
           bh[nt][k] = transpose_8x8(hi);
-          bl[nt][k] = transpose_8x8(pack_bf162(d[nt][2 * k] - bf16x2_lo(hi), d[nt][2 * k + 1] - bf16x2_hi(hi)));
+          bl[nt][k] = transpose_8x8(pack_bf162(d[0][nt][2 * k] - bf16x2_lo(hi), d[0][nt][2 * k + 1] - bf16x2_hi(hi)));
         }
       const uint16_t* sv[4];
       bool on[4];
