@@ -42,7 +42,7 @@ struct KvAttn {
 //
 // An item is (request, row tile, kv head): a row tile is kRows consecutive
 // (token, query head) rows of a request, row = token * G + g.  An item's keys are
-// cut into units (64 encoded tokens, or 64 window tokens).  An item costs its units
+// cut into units (64 encoded tokens, or kWinUnit window tokens).  An item costs its units
 // and what beginning and ending it takes (rotations, the row's output), counted in
 // units.  All items' costs in order, 0 .. U - 1, are shared out evenly over the
 // grid's CTAs in contiguous ranges, whatever the requests' lengths are: one long
@@ -52,7 +52,7 @@ struct KvAttn {
 // works its share out for itself: no plan is made beforehand and the host needs
 // no lengths.  A CTA that begins inside an item leaves a note for the join.
 
-constexpr int kUnit = 64;  // tokens per unit
+constexpr int kUnit = 64;  // encoded tokens per unit
 
 constexpr int64_t kMaxKeys = INT32_MAX - 4096;  // key positions are 32-bit below
 
@@ -70,7 +70,7 @@ struct KvItem {
 
 // The pair (request, row tile) number `pair`; units = 0 where it has no rows.
 // (T * q_heads and key positions are below 2^31: checked by the host and here.)
-template <int kRows, int kItemCost>
+template <int kRows, int kWinUnit, int kItemCost>
 __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, bool& bad) {
   KvItem it;
   it.b = tiles == 1 ? pair : pair / tiles;
@@ -94,14 +94,14 @@ __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, 
   it.e_lim = min(max(0, it.p + it.n - static_cast<int>(a.R)), sees);
   it.w_lim = sees;
   it.e_units = (it.e_lim + kUnit - 1) / kUnit;
-  it.units = it.e_units + (it.w_lim - it.e_lim + kUnit - 1) / kUnit;
+  it.units = it.e_units + (it.w_lim - it.e_lim + kWinUnit - 1) / kWinUnit;
   it.cost = static_cast<int64_t>(it.units + kItemCost) * a.H;
   return it;
 }
 
 // The total of all costs; `mine0` = the cost before this thread's pairs.  Called
 // by all kThreads threads of the CTA.
-template <int kRows, int kItemCost, int kThreads>
+template <int kRows, int kWinUnit, int kItemCost, int kThreads>
 __device__ __forceinline__ int64_t kv_total_cost(const KvAttn& a, int tiles, int64_t* warp_sums, int64_t& mine0) {
   const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -111,9 +111,9 @@ __device__ __forceinline__ int64_t kv_total_cost(const KvAttn& a, int tiles, int
   for (int i = 0; i < per; ++i) {
     const int pair = threadIdx.x * per + i;
     if (pair >= pairs) break;
-    sum += kv_item<kRows, kItemCost>(a, pair, tiles, bad).cost;
+    sum += kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad).cost;
   }
-  if (bad && blockIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+  if (bad) raise_device_error(HLWQ_DEVERR_KV_RANGE);
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -134,7 +134,7 @@ __device__ __forceinline__ int64_t kv_total_cost(const KvAttn& a, int tiles, int
 
 // After kv_total_cost: the pair holding cost `want`, found by the thread whose
 // pairs contain it and published in found[0] (pair) and found[1] (where its cost begins).
-template <int kRows, int kItemCost, int kThreads>
+template <int kRows, int kWinUnit, int kItemCost, int kThreads>
 __device__ __forceinline__ void kv_find(const KvAttn& a, int tiles, int64_t mine0, int64_t want, int64_t* found) {
   const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
   int64_t u = mine0;
@@ -144,7 +144,7 @@ __device__ __forceinline__ void kv_find(const KvAttn& a, int tiles, int64_t mine
     for (int i = 0; i < per; ++i) {
       const int pair = threadIdx.x * per + i;
       if (pair >= pairs) break;
-      const int64_t n = kv_item<kRows, kItemCost>(a, pair, tiles, bad).cost;
+      const int64_t n = kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad).cost;
       if (want < u + n) {
         found[0] = pair;
         found[1] = u;
@@ -162,32 +162,45 @@ struct KvCut {
   int count, b, h, row0;
 };
 
-__device__ __forceinline__ int64_t kv_share(int64_t U, int c, int ctas) { return U * c / ctas; }
+// The shares of the cost U of n CTAs (or CTA pairs), this one being number i: each
+// that has one has a cost of at least 1.
+struct KvShares {
+  int64_t U;
+  int i, ctas;
+  __device__ __forceinline__ KvShares(int64_t total, int me, int n) : U(total), i(me) {
+    ctas = static_cast<int>(min(U, static_cast<int64_t>(n)));
+  }
+  __device__ __forceinline__ int64_t operator()(int c) const { return U * c / ctas; }  // where CTA c's share begins
+  // the number of CTAs whose share begins before cost u
+  __device__ __forceinline__ int before(int64_t u) const {
+    return static_cast<int>(min((u * ctas + U - 1) / U, static_cast<int64_t>(ctas)));
+  }
+};
 
 // One after another, the segments (item, range of its units) of a CTA's share
 // [u0, u1) of the cost.  An item's first kItemCost are its beginning and end, then
 // comes a unit at each step: a boundary among the first ones cuts nothing.
-template <int kRows, int kItemCost>
+template <int kRows, int kWinUnit, int kItemCost>
 struct KvWalk {
   int64_t u0, u, u1, at;  // share, where the walk is, where the pair's cost begins
   int pair;
   KvItem it;
   int h, ta, tb, e_tb;    // the segment: kv head, units [ta, tb), encoded ones [ta, e_tb)
 
-  __device__ __forceinline__ void begin(const KvAttn& a, int tiles, int64_t U, int ctas, const int64_t* found) {
-    u = u0 = kv_share(U, blockIdx.x, ctas);
-    u1 = kv_share(U, blockIdx.x + 1, ctas);
+  __device__ __forceinline__ void begin(const KvAttn& a, int tiles, const KvShares& share, const int64_t* found) {
+    u = u0 = share(share.i);
+    u1 = share(share.i + 1);
     pair = static_cast<int>(found[0]);
     at = found[1];
     bool bad = false;
-    it = kv_item<kRows, kItemCost>(a, pair, tiles, bad);
+    it = kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad);
   }
   __device__ __forceinline__ bool next(const KvAttn& a, int tiles) {
     bool bad = false;
     while (u < u1) {
       while (u >= at + it.cost) {
         at += it.cost;
-        it = kv_item<kRows, kItemCost>(a, ++pair, tiles, bad);
+        it = kv_item<kRows, kWinUnit, kItemCost>(a, ++pair, tiles, bad);
       }
       const int each = it.units + kItemCost;
       h = static_cast<int>((u - at) / each);
@@ -203,14 +216,13 @@ struct KvWalk {
   }
   // The note for the join when this is the share's first segment and begins
   // inside its item: whether the boundary before this CTA is the item's first cut.
-  __device__ __forceinline__ bool note(const KvAttn&, int64_t U, int ctas, KvCut& cut) const {
+  __device__ __forceinline__ bool note(const KvShares& share, KvCut& cut) const {
     const int each = it.units + kItemCost;
     const int64_t s0 = at + static_cast<int64_t>(h) * each, s1 = s0 + each;
     if (ta == 0 || u0 <= s0) return false;
-    if (kv_share(U, blockIdx.x - 1, ctas) > s0 + kItemCost) return false;
+    if (share(share.i - 1) > s0 + kItemCost) return false;
     // parts: the CTA before this one, this one, and those that begin before the item's end
-    cut = {1 + static_cast<int>(min((s1 * ctas + U - 1) / U, static_cast<int64_t>(ctas))) - static_cast<int>(blockIdx.x), it.b,
-           h, it.row0};
+    cut = {1 + share.before(s1) - share.i, it.b, h, it.row0};
     return true;
   }
 };
@@ -347,7 +359,10 @@ constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
 constexpr int kStage = 3136;  // 16 keys: K codes 1536, V codes 1536, K norms 32, V norms 32
 constexpr int kStages = 4;
-constexpr int kRowItemCost = 2;
+// An item's beginning and end (rotations, joining the warps) take about 6 us where a
+// unit takes 1.3; a window tile of 16 about as long as a unit.
+constexpr int kRowItemCost = 5;
+constexpr int kRowWinUnit = 16;
 constexpr int kTabBytes = 64 * 128;
 constexpr float kMinM = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -421,20 +436,20 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     reinterpret_cast<uint32_t*>(gtab)[i] = pack_half2(__ldg(a.codebook + ((i >> 5) & 7)), __ldg(a.codebook + (i >> 8)));
 
   int64_t mine0;
-  const int64_t U = kv_total_cost<C::kRows, kRowItemCost, kRowThreads>(a, tiles, warp_sums, mine0);
+  const int64_t U = kv_total_cost<C::kRows, kRowWinUnit, kRowItemCost, kRowThreads>(a, tiles, warp_sums, mine0);
   if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
-  const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));  // every one of these has a share
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  kv_find<C::kRows, kRowItemCost, kRowThreads>(a, tiles, mine0, kv_share(U, blockIdx.x, ctas), found);
-  KvWalk<C::kRows, kRowItemCost> w;
-  w.begin(a, tiles, U, ctas, found);
+  const KvShares share(U, blockIdx.x, gridDim.x);
+  if (share.i >= share.ctas) return;
+  kv_find<C::kRows, kRowWinUnit, kRowItemCost, kRowThreads>(a, tiles, mine0, share(share.i), found);
+  KvWalk<C::kRows, kRowWinUnit, kRowItemCost> w;
+  w.begin(a, tiles, share, found);
 
   while (w.next(a, tiles)) {
     const KvItem& it = w.it;
     const int h = w.h, ta = w.ta, tb = w.tb, nrows = it.nrows;
     if (threadIdx.x == 0) {
       KvCut cut;
-      if (w.note(a, U, ctas, cut)) cuts[blockIdx.x] = cut;
+      if (w.note(share, cut)) cuts[blockIdx.x] = cut;
     }
 
     // rotate the tile's rows into matrix-instruction order
@@ -715,8 +730,8 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
     // ---- window keys, 16 at a time and as they are: bf16 operands, scores exact to
     // fp32, p in two bf16 parts (16 bits)
-    const int w_first = it.e_lim + (max(ta, it.e_units) - it.e_units) * kUnit;
-    const int w_end = min(it.e_lim + (tb - it.e_units) * kUnit, it.w_lim);
+    const int w_first = it.e_lim + (max(ta, it.e_units) - it.e_units) * kRowWinUnit;
+    const int w_end = min(it.e_lim + (tb - it.e_units) * kRowWinUnit, it.w_lim);
     if (w_first < w_end) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) qm[nt][0] = qm[nt][1] = a.scale * kLog2e;
@@ -871,15 +886,15 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 // takes rows of the item that attention CTA c + 1 noted as first cut at its
 // beginning: part 0 is CTA c's last one, part j > 0 CTA c + j's first one.
 // Few-row tiles have many parts: one row per CTA, eight warps take its parts in
-// turn.  128-row tiles have few: a warp per row.  A lane holds eight dims.
+// turn.  Large tiles have few: a warp per row.  A lane holds eight dims.
 constexpr int kJoinThreads = 256;
 template <int kRows>
 struct JoinCfg {
-  static constexpr int kSplit = kRows == 128 ? 1 : 8;              // warps per row
+  static constexpr int kSplit = kRows >= 128 ? 1 : 8;              // warps per row
   static constexpr int kPerCta = kJoinThreads / 32 / kSplit;       // rows per CTA
   static constexpr int kPart = kRows * (kKvDim + 2);
-  // float4 c of row r: row after row, or (128 rows) column after column
-  static __device__ __forceinline__ int at(int r, int c) { return kRows == 128 ? c * kRows + r : r * (kKvDim / 4) + c; }
+  // float4 c of row r: row after row, or (128 rows and more) column after column
+  static __device__ __forceinline__ int at(int r, int c) { return kRows >= 128 ? c * kRows + r : r * (kKvDim / 4) + c; }
 };
 
 template <int kRows>

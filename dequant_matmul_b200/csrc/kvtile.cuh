@@ -4,25 +4,30 @@
 // cores (sm_100a).  The mathematics, the sharing of the work and the join are
 // those of kvattn.cuh.
 //
-// A CTA works on one row tile at a time.  Tensor memory: O [128 x 256] fp32 in
+// A CTA works on one row tile at a time; where a request has more than 128 rows
+// (kPair), two CTAs work on a tile of 256, each on half the rows: the MMAs take a
+// K tile of which each CTA holds (and decodes) half the keys, and a V^T tile of which
+// each holds half the dims, so every code is decoded once for 256 rows
+// (cta_group::2; the first CTA issues them, the second one's warps report to its barriers).  Tensor memory: O [128 x 256] fp32 in
 // columns 0..255, the rotated rows Q [128 x 256] binary16 in 256..383, two score
 // tiles S [128 x 64] fp32 in 384..511, each overwritten by its P (binary16, 32
 // columns).  Q and P are the A operands (so shared memory carries only what is
 // decoded); K [64 keys][256 dims] and V^T [256 dims][64 keys] are the B operands,
 // both K-major with the 128-byte swizzle, decoded there from the 3-bit codes.
 //
-// Roles (18 warps):
+// Roles (19 warps):
 //   0..7   softmax: two threads per row (warps q and q + 4 of tensor-memory quarter
 //          q), half the columns each.  They put Q into tensor memory (rotated in
 //          two passes over the columns of O, which are free then), turn S(j) into
 //          P(j), rescale O when a row's reference rises (seldom, as in the few-row
 //          kernel; one reducing barrier of the two warps finds out), rotate O back
 //          and write the rows.
-//   8..15  decode: code pairs -> binary16 pairs through the 64-entry table (one
+//   8..15  decode (a pair's CTA: four warps K, four V): code pairs -> binary16 pairs through the 64-entry table (one
 //          copy per lane) -> 16-byte stores into the K and V^T tiles; window
 //          tiles are copied (K) and transposed (V) as they are, bf16.
-//   16     issues the MMAs: S(j + 1), then O += P(j) V(j).
-//   17     fetches codes and norms, 16 keys (never two pages) per bulk copy.
+//   16, 17 issue the MMAs, one S(j), one O += P(j) V(j): a 64-column MMA takes three
+//          times as long to issue as to run, so the two products have a thread each.
+//   18     fetches codes and norms, 16 keys (never two pages) per bulk copy.
 //
 // Keys stand in the tiles in an order that keeps every shared-memory access of
 // the decoders free of bank conflicts: row n = 8 w + g of the K tile is key
@@ -30,10 +35,10 @@
 // rows is the same key; P's columns follow by picking registers.  The 16-key
 // groups of a stage are 16 bytes further apart than their contents for the same reason.
 //
-// What bounds it: shared memory.  Per tile of 64 keys the table reads, the
-// stores, the staging and the norms take about 1400 cycles of the SM's
-// 128 bytes per cycle, the MMAs' B operands 512 more, against 1024 cycles of
-// matrix work.
+// What bounds it: shared memory.  A single CTA's table reads, stores and staging
+// take about 1900 cycles of the SM's 128 bytes per cycle for a tile of 64 keys, the
+// MMAs' B operands 512 more, against 1024 cycles of matrix work (2800 cycles measured);
+// in a pair each CTA has half of that.
 //
 // Every wait is bounded (wait_limit_ns from its own beginning), after which the
 // kernel raises HLWQ_DEVERR_TIMEOUT, drains its copies and MMAs and frees its
@@ -49,15 +54,16 @@ namespace hlwq {
 namespace {
 
 constexpr int kAtRows = 128;
-constexpr int kAtWarps = 18, kAtThreads = 32 * kAtWarps;
-constexpr int kAtDec0 = 8, kAtMma = 16;
+constexpr int kAtWarps = 19, kAtThreads = 32 * kAtWarps;
+constexpr int kAtDec0 = 8, kAtMma = 16, kAtPv = 17;
+constexpr int kAtWinUnit = 64;
 constexpr int kAtItemCost = 8;                       // units: an item takes about 12 us besides its tiles of 1.5 us
 constexpr int kGrp = 1536 + 16;                      // 16 keys' codes, and the gap
 constexpr int kCodeStage = 12800;                    // K codes, V codes, norms [2][64] binary16, mask
 constexpr int kCodeStages = 3;
 constexpr int kNormOff = 2 * 4 * kGrp;               // 12416
 constexpr int kMaskOff = kNormOff + 256;
-constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
+constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile (a pair's CTA uses half)
 constexpr int kNrmSlot = 128 * 4 + 16;               // K norms, V norms, maxima of V's, mask
 constexpr float kMinQm = 1e-36f;                     // a zero scale: masked keys (-inf) stay masked, the others equal
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
@@ -71,23 +77,34 @@ __host__ __device__ constexpr int at_key(int n) {
   return 16 * (n & 3) + 2 * ((n >> 2) & 1) + ((n >> 3) & 1) + 4 * (n >> 4);
 }
 
-// Instruction descriptor: kind::f16 with binary16 or bfloat16 operands, K-major, D fp32, M = 128.
-__host__ __device__ constexpr uint32_t idesc_16(int n, bool bf16) {
-  return idesc_f16(n) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+// Instruction descriptor: kind::f16 with binary16 or bfloat16 operands, K-major, D fp32,
+// M = 128 (256 for a pair).
+__host__ __device__ constexpr uint32_t idesc_16(int n, bool bf16, bool pair) {
+  return idesc_f16(n) + (pair ? static_cast<uint32_t>(128 >> 4) << 24 : 0u) + (bf16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Bounded wait whose limit starts when it has to wait.
+// Bounded wait whose limit starts when it has to wait; kCluster: for the other CTA's arrivals.
+template <bool kCluster = false>
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity) {
   uint64_t deadline = 0;
   for (uint32_t n = 1;; ++n) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (kCluster)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
     if (ok) return true;
     if ((n & 63u) == 0u) {
       const uint64_t t = globaltimer_ns();
@@ -95,6 +112,57 @@ __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity) {
       else if (t > deadline) return false;
     }
   }
+}
+
+// A pair's second CTA reports to the first one's MMA issuers: one thread waits for
+// its own CTA's warps (cta scope, cheap for them) and passes it on at cluster scope,
+// once; with every warp arriving at cluster scope itself each tile waits
+// for the warps' own stores (1.2 times the time).
+__device__ __forceinline__ void report(uint32_t bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void at_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else tc_mma_f16(d_tmem, a_tmem, b_desc, idesc, accumulate);
+}
+
+// The MMAs issued so far arrive at this barrier (of both CTAs) when they are done.
+template <bool kPair>
+__device__ __forceinline__ void at_commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else tc_commit(bar);
+}
+
+// No MMA may be under way when the tensor memory is freed: an issuer that gives up
+// waits for the ones it has issued, on a barrier of its own.
+template <bool kPair>
+__device__ __forceinline__ void drain_mma(uint32_t bar) {
+  mbar_init(bar, 1);
+  fence_barrier_init();
+  if constexpr (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else tc_commit(bar);
+  at_wait(bar, 0);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The same for a whole warp: all lanes or none.
@@ -231,6 +299,7 @@ __device__ __forceinline__ void across_blocks(uint32_t row, int half, F&& f) {
   tc_wait_st();
 }
 
+template <bool kPair>
 __global__ void __launch_bounds__(kAtThreads, 1)
 kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut* __restrict__ cuts) {
   extern __shared__ __align__(16) uint8_t asm_raw[];
@@ -243,18 +312,21 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   const uint32_t nrm = codes + kCodeStages * kCodeStage, bars = nrm + 4 * kNrmSlot;
   const uint32_t c_full = bars, c_empty = c_full + 8 * kCodeStages, k_full = c_empty + 8 * kCodeStages, k_empty = k_full + 16,
                  v_full = k_empty + 16, v_empty = v_full + 16, s_full = v_empty + 16, p_full = s_full + 16,
-                 q_full = p_full + 16, o_done = q_full + 8, misc = o_done + 8;
+                 q_full = p_full + 16, k_peer = q_full + 8, vp_peer = k_peer + 16,
+                 q_peer = vp_peer + 16, misc = q_peer + 8;
   volatile uint32_t* misc_g = reinterpret_cast<volatile uint32_t*>(g0 + (misc - tab0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kRows = kPair ? 2 * kAtRows : kAtRows, kHalf = kPair ? 2 : 1;
+  const int rank = kPair ? blockIdx.x & 1 : 0, me = blockIdx.x / kHalf;  // (clusters are consecutive CTAs)
 
-  if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
+  if (threadIdx.x == 0 && rank == 0) cuts[me] = {0, 0, 0, 0};
   int64_t mine0;
-  const int64_t U = kv_total_cost<kAtRows, kAtItemCost, kAtThreads>(a, tiles, warp_sums, mine0);
-  const int ctas = static_cast<int>(min(U, static_cast<int64_t>(gridDim.x)));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;  // before any barrier or tensor memory
-  kv_find<kAtRows, kAtItemCost, kAtThreads>(a, tiles, mine0, kv_share(U, blockIdx.x, ctas), found);
-  KvWalk<kAtRows, kAtItemCost> w;
-  w.begin(a, tiles, U, ctas, found);
+  const int64_t U = kv_total_cost<kRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, warp_sums, mine0);
+  const KvShares share(U, me, gridDim.x / kHalf);
+  if (me >= share.ctas) return;  // (both of a pair) before any barrier or tensor memory
+  kv_find<kRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, mine0, share(me), found);
+  KvWalk<kRows, kAtWinUnit, kAtItemCost> w;
+  w.begin(a, tiles, share, found);
 
   kv_check_codebook(a.codebook);
   for (int i = threadIdx.x; i < 64 * 32; i += kAtThreads)
@@ -265,23 +337,31 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       mbar_init(c_empty + 8 * s, 8);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(k_full + 8 * s, 8);
+      mbar_init(k_full + 8 * s, 8 / kHalf);  // the decode warps that write it
       mbar_init(k_empty + 8 * s, 1);
-      mbar_init(v_full + 8 * s, 8);
+      mbar_init(v_full + 8 * s, 8 / kHalf);
       mbar_init(v_empty + 8 * s, 1);
       mbar_init(s_full + 8 * s, 1);
       mbar_init(p_full + 8 * s, 8);
+      mbar_init(k_peer + 8 * s, 1);          // the second CTA's reports
+      mbar_init(vp_peer + 8 * s, 1);
     }
+    mbar_init(q_peer, 1);
     mbar_init(q_full, 8);
-    mbar_init(o_done, 1);
     fence_barrier_init();
   }
   if (warp == kAtMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // the barriers and the tensor memory of both are there
   tc_fence_after();
   const uint32_t tmem = misc_g[0];
   bool ok = true;
@@ -290,21 +370,23 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   // Ring slot and parity of tile j: j % 2 and (j / 2) & 1.
   if (warp < kAtDec0) {
     // ------------------------------------------------------------ softmax
-    const int half = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;  // r: row of the tile
+    const int half = warp >> 2, quarter = warp & 3, r0 = 32 * quarter + lane, r = kAtRows * rank + r0;  // r: row of the tile
     const uint32_t row = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float sgn = a.scale < 0.0f ? -1.0f : 1.0f;
-    float* mine = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + half * kAtRows + r;        // exchange with the
-    const float* other = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + (half ^ 1) * kAtRows + r;  // row's other thread
+    float* mine = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + half * kAtRows + r0;       // exchange with the
+    const float* other = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + (half ^ 1) * kAtRows + r0;  // row's other thread
     uint32_t gt = 0;
+    // the product of tile j has been added to O (tile j - 2's was before S(j) came)
+    auto pv_done = [&](uint32_t j) { return at_wait_warp(v_empty + 8 * (j & 1u), (j >> 1) & 1u); };
     while (ok && w.next(a, tiles)) {
       const KvItem& it = w.it;
       const bool on = r < it.nrows;
       const int tr = it.row0 + (on ? r : 0), tok = tr / a.G, head = w.h * a.G + (tr - tok * a.G);
       const uint16_t* qrow = a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + head * kKvDim;
       const int lim = on ? it.p + tok + 1 : 0;
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && rank == 0) {
         KvCut cut;
-        if (w.note(a, U, ctas, cut)) cuts[blockIdx.x] = cut;
+        if (w.note(share, cut)) cuts[me] = cut;
       }
       // m: the row's reference; lf: log2 of the power of two that keeps p n in
       // binary16's range, in l as in O; l: this thread's share of the row's sum
@@ -383,7 +465,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         if (fix) {
           l *= corr;
           if (started) {  // rescale O once the product before has been added
-            if (pair_any(quarter, !at_wait_warp(o_done, (gt - 1) & 1u))) return false;
+            if (pair_any(quarter, !pv_done(gt - 1))) return false;
 #pragma unroll 1
             for (int c = 128 * half; c < 128 * half + 128; c += 16) {
               uint32_t x[16];
@@ -489,7 +571,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         for (int t = w.ta; ok && t < w.e_tb; ++t) ok = tile(std::false_type{}, t * kUnit, it.e_lim);
-        if (!ok || pair_any(quarter, !at_wait_warp(o_done, (gt - 1) & 1u))) {
+        if (!ok || pair_any(quarter, !pv_done(gt - 1))) {
           ok = false;
           break;
         }
@@ -529,8 +611,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        for (int t = w.e_tb; ok && t < w.tb; ++t) ok = tile(std::true_type{}, it.e_lim + (t - it.e_units) * kUnit, it.w_lim);
-        if (!ok || pair_any(quarter, !at_wait_warp(o_done, (gt - 1) & 1u))) {
+        for (int t = w.e_tb; ok && t < w.tb; ++t) ok = tile(std::true_type{}, it.e_lim + (t - it.e_units) * kAtWinUnit, it.w_lim);
+        if (!ok || pair_any(quarter, !pv_done(gt - 1))) {
           ok = false;
           break;
         }
@@ -542,7 +624,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       const bool whole = w.ta == 0 && w.tb == it.units;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       uint16_t* orow = a.out + static_cast<int64_t>(it.c0 + tok) * a.ldo + head * kKvDim;
-      float* part = parts + static_cast<int64_t>(2 * blockIdx.x + (w.ta == 0 ? 1 : 0)) * (kAtRows * (kKvDim + 2));
+      float* part = parts + static_cast<int64_t>(2 * me + (w.ta == 0 ? 1 : 0)) * (kRows * (kKvDim + 2));
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 16) {
         uint32_t x[16];
@@ -560,25 +642,29 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         } else if (on) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // [256 columns / 4][row][4]: a warp writes 512 bytes at a time
-            reinterpret_cast<uint4*>(part)[(c / 4 + k) * kAtRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            reinterpret_cast<uint4*>(part)[(c / 4 + k) * kRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
         __syncwarp();
       }
       if (!whole && on && half == 0) {
-        part[kAtRows * kKvDim + r] = m;
-        part[kAtRows * (kKvDim + 1) + r] = l;
+        part[kRows * kKvDim + r] = m;
+        part[kRows * (kKvDim + 1) + r] = l;
       }
       pair_sync(quarter);  // O, Q and the exchange words are free for the next segment
     }
   } else if (warp < kAtMma) {
     // ------------------------------------------------------------ decode
-    const int dw = warp - kAtDec0, g = lane & 7, t4 = lane >> 3, tid = threadIdx.x - 32 * kAtDec0;
+    // dl: this warp's place among those that decode K, or V, in this CTA; dw: in the whole tile
+    const int g = lane & 7, t4 = lane >> 3, tid = threadIdx.x - 32 * kAtDec0;
+    const bool do_k = !kPair || warp < kAtDec0 + 4, do_v = !kPair || !do_k;
+    const int dl = kPair ? (warp - kAtDec0) & 3 : warp - kAtDec0, dw = dl + 4 * rank;
+    constexpr int kSlab = 8192 / kHalf;  // K tile: rows x 64 dims
     const uint32_t tab = tab0 + 4 * lane;
     uint32_t gt = 0, ce = 0;
     while (ok && w.next(a, tiles)) {
       for (int t = w.ta; ok && t < w.e_tb; ++t, ++gt, ++ce) {
         const uint32_t cs = ce % kCodeStages, st = codes + cs * kCodeStage, s = gt & 1u, par = (gt >> 1) & 1u;
-        ok = at_wait_warp(c_full + 8 * cs, (ce / kCodeStages) & 1u) && at_wait_warp(k_empty + 8 * s, par ^ 1u);
+        ok = at_wait_warp(c_full + 8 * cs, (ce / kCodeStages) & 1u) && (!do_k || at_wait_warp(k_empty + 8 * s, par ^ 1u));
         if (!ok) break;
         const uint32_t there = lds32(st + kMaskOff);
         const int left = w.it.e_lim - t * kUnit;  // keys from here to the end
@@ -590,10 +676,10 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           const uint32_t slot = nrm + (gt & 3u) * kNrmSlot;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + 4 * tid), "f"(x) : "memory");
           const uint32_t mx = __reduce_max_sync(0xffffffffu, x == x ? __float_as_uint(x) : 0u);
-          if (dw >= 2 && lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 512 + 4 * (dw - 2)), "r"(mx) : "memory");
+          if (tid >= 64 && lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 512 + 4 * ((tid - 64) >> 5)), "r"(mx) : "memory");
           if (tid == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 520), "r"(there) : "memory");
         }
-        {  // K: key of row 8 dw + g, dims 64 t4 .. + 63
+        if (do_k) {  // K: key of row 8 dw + g, dims 64 t4 .. + 63
           const uint32_t src = st + (g & 3) * kGrp + (2 * (g >> 2) + (dw & 1) + 4 * (dw >> 1)) * kKvBytes + 24 * t4;
           uint32_t x[6];
 #pragma unroll
@@ -601,7 +687,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             const uint2 y = lds64(src + 8 * i);
             x[2 * i] = y.x, x[2 * i + 1] = y.y;
           }
-          const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
+          const uint32_t dst = k_tiles + s * kKvTile + kSlab * t4 + (8 * dl + g) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t h[4];
@@ -616,13 +702,14 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             }
             sts128(dst + ((c ^ g) << 4), h[0], h[1], h[2], h[3]);
           }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full + 8 * s);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + 8 * s);
-        ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
-        if (!ok) break;
-        {  // V^T: places 8 g .. + 7, dims 8 (4 dw + t4) .. + 7: 24 bits of each of eight keys
+        if (do_v) {
+          ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
+          if (!ok) break;
+          // V^T: places 8 g .. + 7, dims 8 (4 dw + t4) .. + 7: 24 bits of each of eight keys
           const uint32_t src = st + 4 * kGrp + (g & 3) * kGrp + 2 * (g >> 2) * kKvBytes + 12 * dw + 4 * ((24 * t4) >> 5);
           uint32_t x[8];
 #pragma unroll
@@ -630,7 +717,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             const uint32_t at = src + ((i & 1) + 4 * (i >> 1)) * kKvBytes;
             x[i] = __funnelshift_r(lds32(at), lds32(at + 4), (24 * t4) & 31);
           }
-          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
+          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dl + t4) * 128;
           constexpr uint32_t kEven = 0x1c71c7u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // even and odd codes of two keys side by side
@@ -649,39 +736,37 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             }
             sts128(dst + c * 128 + ((g ^ c) << 4), h[0], h[1], h[2], h[3]);
           }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full + 8 * s);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(v_full + 8 * s);
-          mbar_arrive(c_empty + 8 * cs);
-        }
+        if (lane == 0) mbar_arrive(c_empty + 8 * cs);
       }
       if (!ok) break;
       const int R = static_cast<int>(a.R);
       const int64_t ring = (static_cast<int64_t>(w.it.b) * a.H + w.h) * R;
       for (int t = w.e_tb; ok && t < w.tb; ++t, ++gt) {
         const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
-        const int k0 = w.it.e_lim + (t - w.it.e_units) * kUnit, end = w.it.w_lim;
-        ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
-        if (!ok) break;
-        {
+        const int k0 = w.it.e_lim + (t - w.it.e_units) * kAtWinUnit, end = w.it.w_lim;
+        if (do_k) {
+          ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
+          if (!ok) break;
           const int key = k0 + at_key(8 * dw + g);
           const uint4* src = reinterpret_cast<const uint4*>(a.kwin + (ring + (key < end ? key % R : 0)) * kKvDim + 64 * t4);
-          const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
+          const uint32_t dst = k_tiles + s * kKvTile + kSlab * t4 + (8 * dl + g) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (key < end) x = __ldg(src + c);
             sts128(dst + ((c ^ g) << 4), x.x, x.y, x.z, x.w);
           }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full + 8 * s);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + 8 * s);
-        ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
-        if (!ok) break;
-        {
+        if (do_v) {
+          ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
+          if (!ok) break;
           uint32_t x[8][4];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -690,7 +775,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             if (key < end) y = __ldg(reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 8 * (4 * dw + t4)));
             x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
           }
-          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
+          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dl + t4) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t h[4];
@@ -698,81 +783,93 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             for (int i = 0; i < 4; ++i) h[i] = __byte_perm(x[2 * i][c >> 1], x[2 * i + 1][c >> 1], (c & 1) ? 0x7632 : 0x5410);
             sts128(dst + c * 128 + ((g ^ c) << 4), h[0], h[1], h[2], h[3]);
           }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full + 8 * s);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + 8 * s);
       }
     }
+    if (ok) {  // the last commits' arrivals land before the CTA ends
+      const uint32_t s = (gt - 1) & 1u, par = ((gt - 1) >> 1) & 1u;
+      ok = (!do_k || at_wait_warp(k_empty + 8 * s, par)) && (!do_v || at_wait_warp(v_empty + 8 * s, par));
+    }
   } else if (warp == kAtMma) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer: S
+    // (in a pair's second CTA these loops pass its readiness on to the first one)
     if (lane == 0) {
       uint32_t gt = 0, nq = 0;
-      // O (+)= P(j) V(j)
-      auto pv = [&](uint32_t j, bool win, bool first) -> bool {
-        const uint32_t s = j & 1u, par = (j >> 1) & 1u;
-        if (!at_wait(v_full + 8 * s, par) || !at_wait(p_full + 8 * s, par)) return false;
-        tc_fence_after();
-        const uint64_t desc = smem_desc_sw128(v_tiles + s * kKvTile);
-        const uint32_t id = idesc_16(256, win);
-        for (int part = 0; part < (win ? 2 : 1); ++part)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_f16(tmem + kColO, tmem + kColS + 64 * s + 32 * part + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
-                       first && part == 0 && k == 0 ? 0u : 1u);
-        tc_commit(v_empty + 8 * s);
-        tc_commit(o_done);
-        return true;
-      };
       while (ok && w.next(a, tiles)) {
-        bool first = true;
         for (int phase = 0; ok && phase < 2; ++phase) {
           const bool win = phase == 1;
           const int n = win ? w.tb - w.e_tb : w.e_tb - w.ta;
           if (n == 0) continue;
           ok = at_wait(q_full, nq & 1u);
+          if (ok && kPair) {
+            if (rank) {
+              tc_fence_after();
+              tc_fence_before();
+              report(q_peer);
+            }
+            else ok = at_wait<true>(q_peer, nq & 1u);
+          }
           ++nq;
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t id = idesc_16(64, win);
+          const uint32_t id = idesc_16(64, win, kPair);
           for (int t = 0; ok && t < n; ++t, ++gt) {
             const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
+            // S(gt)'s columns were P(gt - 2): v_empty says that its product is done
             ok = at_wait(k_full + 8 * s, par);
+            if (ok && rank) {
+              report(k_peer + 8 * s);
+              continue;
+            }
+            ok = ok && at_wait(v_empty + 8 * s, par ^ 1u) && (!kPair || at_wait<true>(k_peer + 8 * s, par));
             if (!ok) break;
             tc_fence_after();
-            // S(gt)'s columns were P(gt - 2): its product was issued before
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint64_t desc = smem_desc_sw128(k_tiles + s * kKvTile + 8192 * c);
+              const uint64_t desc = smem_desc_sw128(k_tiles + s * kKvTile + 8192 / kHalf * c);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                tc_mma_f16(tmem + kColS + 64 * s, tmem + kColQ + 32 * c + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
-                           c || k ? 1u : 0u);
+                at_mma<kPair>(tmem + kColS + 64 * s, tmem + kColQ + 32 * c + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
+                              c || k ? 1u : 0u);
             }
-            tc_commit(k_empty + 8 * s);
-            tc_commit(s_full + 8 * s);
-            if (t > 0) {
-              ok = pv(gt - 1, win, first);
-              first = false;
-            }
-          }
-          if (ok) {
-            ok = pv(gt - 1, win, first);
-            first = false;
+            at_commit<kPair>(k_empty + 8 * s);
+            at_commit<kPair>(s_full + 8 * s);
           }
         }
       }
-      if (ok && gt > 0) {  // the last commits' arrivals land before the CTA ends
-        at_wait(k_empty + 8 * ((gt - 1) & 1u), ((gt - 1) >> 1) & 1u);
-        at_wait(v_empty + 8 * ((gt - 1) & 1u), ((gt - 1) >> 1) & 1u);
+      if (!ok && rank == 0) drain_mma<kPair>(misc + 16);
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  } else if (warp == kAtPv) {
+    // ------------------------------------------------------------ MMA issuer: O += P V
+    if (lane == 0) {
+      uint32_t gt = 0;
+      while (ok && w.next(a, tiles)) {
+        const int ne = w.e_tb - w.ta, n = w.tb - w.ta;
+        for (int t = 0; ok && t < n; ++t, ++gt) {
+          const bool win = t >= ne;
+          const uint32_t s = gt & 1u, par = (gt >> 1) & 1u, id = idesc_16(256, win, kPair);
+          ok = at_wait(v_full + 8 * s, par) && at_wait(p_full + 8 * s, par);
+          if (ok && rank) {
+            tc_fence_after();
+            tc_fence_before();
+            report(vp_peer + 8 * s);
+            continue;
+          }
+          ok = ok && (!kPair || at_wait<true>(vp_peer + 8 * s, par));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t desc = smem_desc_sw128(v_tiles + s * kKvTile);
+          for (int part = 0; part < (win ? 2 : 1); ++part)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              at_mma<kPair>(tmem + kColO, tmem + kColS + 64 * s + 32 * part + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
+                            t == 0 && part == 0 && k == 0 ? 0u : 1u);
+          at_commit<kPair>(v_empty + 8 * s);
+        }
       }
-      if (!ok) {
-        // no MMA may be under way when the tensor memory is freed: one more commit, waited for
-        mbar_init(misc + 16, 1);
-        fence_barrier_init();
-        tc_commit(misc + 16);
-        at_wait(misc + 16, 0);
-      }
+      if (!ok && rank == 0) drain_mma<kPair>(misc + 24);
     }
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   } else {
@@ -822,42 +919,58 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // no arrival and no MMA of the other CTA is under way
   if (warp == kAtMma) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 
-int launch_tiles(const KvAttn& a, int ctas, int tiles, float* parts, KvCut* cuts, cudaStream_t stream) {
+template <bool kPair>
+int launch_tiles(const KvAttn& a, int shares, int tiles, float* parts, KvCut* cuts, cudaStream_t stream) {
   static PerDeviceOnce attr;
   if (const int st = attr([&] {
-        return cudaFuncSetAttribute(kv_attn_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem) ==
+        return cudaFuncSetAttribute(kv_attn_tile_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem) ==
                cudaSuccess;
       }))
     return st;
-  kv_attn_tile_kernel<<<ctas, kAtThreads, kAtSmem, stream>>>(a, tiles, parts, cuts);
-  if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
-  return launch_join<kAtRows>(a, ctas, parts, cuts, stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(shares * (kPair ? 2 : 1));
+  cfg.blockDim = dim3(kAtThreads);
+  cfg.dynamicSmemBytes = kAtSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = kPair ? 2 : 1;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = kPair ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kv_attn_tile_kernel<kPair>, a, tiles, parts, cuts) != cudaSuccess) return HLWQ_ECUDA;
+  return launch_join<kPair ? 2 * kAtRows : kAtRows>(a, shares, parts, cuts, stream);
 }
 
-// Rows per tile, CTAs and row tiles of a request for max_new new tokens: the
-// few-row kernel up to 16 rows per kv head, the tensor-core tiles above.
+// Rows per tile, CTAs (or pairs) that share the work, and row tiles of a request,
+// for max_new new tokens: the few-row kernel up to 16 rows per kv head, above
+// it the tensor-core tiles, in pairs where a request has more than one tile of 128.
 struct KvGrid {
-  int rows, ctas;
+  int rows, shares;
   int64_t tiles;
 };
 inline KvGrid kv_grid(int64_t max_new, int64_t G) {
   const int64_t n = max_new * G;
-  const int rows = n <= 8 ? 8 : n <= 16 ? 16 : kAtRows;
-  return {rows, sm_count() * (rows == 8 ? RowCfg<1>::kCtas : rows == 16 ? RowCfg<2>::kCtas : 1), ceil_div(n, rows)};
+  const int rows = n <= 8 ? 8 : n <= 16 ? 16 : n <= kAtRows ? kAtRows : 2 * kAtRows;
+  const int sms = sm_count();
+  return {rows, rows == 8 ? sms * RowCfg<1>::kCtas : rows == 16 ? sms * RowCfg<2>::kCtas : rows == kAtRows ? sms : sms / 2,
+          ceil_div(n, rows)};
 }
 
 }  // namespace
 
-// Workspace: two partial results per CTA, then a note per CTA for the join.
+// Workspace: two partial results per share, then a note per share for the join.
 size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t Hq, int64_t H) {
   const KvGrid gr = kv_grid(max_new, Hq / H);
-  return static_cast<size_t>(gr.ctas) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
+  return static_cast<size_t>(gr.shares) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
 }
 
 int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
@@ -865,10 +978,13 @@ int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_
   if (gr.tiles * a.B > INT32_MAX) return HLWQ_EUNSUPPORTED;
   const int tiles = static_cast<int>(gr.tiles);
   float* parts = static_cast<float*>(workspace);
-  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.ctas * gr.rows * (kKvDim + 2));
-  return gr.rows == 8    ? launch_rows<1>(a, gr.ctas, tiles, parts, cuts, stream)
-         : gr.rows == 16 ? launch_rows<2>(a, gr.ctas, tiles, parts, cuts, stream)
-                         : launch_tiles(a, gr.ctas, tiles, parts, cuts, stream);
+  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.shares * gr.rows * (kKvDim + 2));
+  switch (gr.rows) {
+    case 8: return launch_rows<1>(a, gr.shares, tiles, parts, cuts, stream);
+    case 16: return launch_rows<2>(a, gr.shares, tiles, parts, cuts, stream);
+    case kAtRows: return launch_tiles<false>(a, gr.shares, tiles, parts, cuts, stream);
+    default: return launch_tiles<true>(a, gr.shares, tiles, parts, cuts, stream);
+  }
 }
 
 }  // namespace hlwq
