@@ -124,17 +124,28 @@ __device__ __forceinline__ void report(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
 }
 
+// MMAs and commits are issued by one elected lane, but in warp-uniform control flow:
+// descriptors and addresses then stay in uniform registers.  Inside a branch of
+// one lane every MMA took about 90 cycles to issue.
 template <bool kPair>
 __device__ __forceinline__ void at_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
   if constexpr (kPair)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-  else tc_mma_f16(d_tmem, a_tmem, b_desc, idesc, accumulate);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // The MMAs issued so far arrive at this barrier (of both CTAs) when they are done.
@@ -142,22 +153,17 @@ template <bool kPair>
 __device__ __forceinline__ void at_commit(uint32_t bar) {
   if constexpr (kPair)
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
         "h"(static_cast<uint16_t>(3))
         : "memory");
-  else tc_commit(bar);
-}
-
-// No MMA may be under way when the tensor memory is freed: an issuer that gives up
-// waits for the ones it has issued, on a barrier of its own.
-template <bool kPair>
-__device__ __forceinline__ void drain_mma(uint32_t bar) {
-  mbar_init(bar, 1);
-  fence_barrier_init();
-  if constexpr (kPair)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-  else tc_commit(bar);
-  at_wait(bar, 0);
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -166,8 +172,28 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The same for a whole warp: all lanes or none.
+template <bool kCluster = false>
 __device__ __forceinline__ bool at_wait_warp(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, at_wait(bar, parity));
+  return __all_sync(0xffffffffu, at_wait<kCluster>(bar, parity));
+}
+
+// No MMA may be under way when the tensor memory is freed: an issuing warp that
+// gives up waits for the ones it has issued, on a barrier of its own.
+template <bool kPair>
+__device__ __forceinline__ void drain_mma(uint32_t bar, int lane) {
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+  else at_commit<false>(bar);
+  at_wait_warp(bar, 0);
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -796,33 +822,33 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   } else if (warp == kAtMma) {
     // ------------------------------------------------------------ MMA issuer: S
     // (in a pair's second CTA these loops pass its readiness on to the first one)
-    if (lane == 0) {
+    {
       uint32_t gt = 0, nq = 0;
       while (ok && w.next(a, tiles)) {
         for (int phase = 0; ok && phase < 2; ++phase) {
           const bool win = phase == 1;
           const int n = win ? w.tb - w.e_tb : w.e_tb - w.ta;
           if (n == 0) continue;
-          ok = at_wait(q_full, nq & 1u);
+          ok = at_wait_warp(q_full, nq & 1u);
           if (ok && kPair) {
             if (rank) {
               tc_fence_after();
               tc_fence_before();
-              report(q_peer);
+              if (lane == 0) report(q_peer);
             }
-            else ok = at_wait<true>(q_peer, nq & 1u);
+            else ok = at_wait_warp<true>(q_peer, nq & 1u);
           }
           ++nq;
           const uint32_t id = idesc_16(64, win, kPair);
           for (int t = 0; ok && t < n; ++t, ++gt) {
             const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
             // S(gt)'s columns were P(gt - 2): v_empty says that its product is done
-            ok = at_wait(k_full + 8 * s, par);
+            ok = at_wait_warp(k_full + 8 * s, par);
             if (ok && rank) {
-              report(k_peer + 8 * s);
+              if (lane == 0) report(k_peer + 8 * s);
               continue;
             }
-            ok = ok && at_wait(v_empty + 8 * s, par ^ 1u) && (!kPair || at_wait<true>(k_peer + 8 * s, par));
+            ok = ok && at_wait_warp(v_empty + 8 * s, par ^ 1u) && (!kPair || at_wait_warp<true>(k_peer + 8 * s, par));
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -838,26 +864,25 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
         }
       }
-      if (!ok && rank == 0) drain_mma<kPair>(misc + 16);
+      if (!ok && rank == 0) drain_mma<kPair>(misc + 16, lane);
     }
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   } else if (warp == kAtPv) {
     // ------------------------------------------------------------ MMA issuer: O += P V
-    if (lane == 0) {
+    {
       uint32_t gt = 0;
       while (ok && w.next(a, tiles)) {
         const int ne = w.e_tb - w.ta, n = w.tb - w.ta;
         for (int t = 0; ok && t < n; ++t, ++gt) {
           const bool win = t >= ne;
           const uint32_t s = gt & 1u, par = (gt >> 1) & 1u, id = idesc_16(256, win, kPair);
-          ok = at_wait(v_full + 8 * s, par) && at_wait(p_full + 8 * s, par);
+          ok = at_wait_warp(v_full + 8 * s, par) && at_wait_warp(p_full + 8 * s, par);
           if (ok && rank) {
             tc_fence_after();
             tc_fence_before();
-            report(vp_peer + 8 * s);
+            if (lane == 0) report(vp_peer + 8 * s);
             continue;
           }
-          ok = ok && (!kPair || at_wait<true>(vp_peer + 8 * s, par));
+          ok = ok && (!kPair || at_wait_warp<true>(vp_peer + 8 * s, par));
           if (!ok) break;
           tc_fence_after();
           const uint64_t desc = smem_desc_sw128(v_tiles + s * kKvTile);
@@ -869,9 +894,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           at_commit<kPair>(v_empty + 8 * s);
         }
       }
-      if (!ok && rank == 0) drain_mma<kPair>(misc + 24);
+      if (!ok && rank == 0) drain_mma<kPair>(misc + 24, lane);
     }
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   } else {
     // ------------------------------------------------------------ loader
     uint32_t ce = 0;
