@@ -162,7 +162,7 @@ struct KvCut {
   int count, b, h, row0;
 };
 
-// The shares of the cost U of n CTAs (or CTA pairs), this one being number i: each
+// The shares of the cost U of n CTAs, this one being number i: each
 // that has one has a cost of at least 1.
 struct KvShares {
   int64_t U;
@@ -886,15 +886,15 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 // takes rows of the item that attention CTA c + 1 noted as first cut at its
 // beginning: part 0 is CTA c's last one, part j > 0 CTA c + j's first one.
 // Few-row tiles have many parts: one row per CTA, eight warps take its parts in
-// turn.  Large tiles have few: a warp per row.  A lane holds eight dims.
+// turn.  128-row tiles have few: a warp per row.  A lane holds eight dims.
 constexpr int kJoinThreads = 256;
 template <int kRows>
 struct JoinCfg {
-  static constexpr int kSplit = kRows >= 128 ? 1 : 8;              // warps per row
+  static constexpr int kSplit = kRows == 128 ? 1 : 8;              // warps per row
   static constexpr int kPerCta = kJoinThreads / 32 / kSplit;       // rows per CTA
   static constexpr int kPart = kRows * (kKvDim + 2);
-  // float4 c of row r: row after row, or (128 rows and more) column after column
-  static __device__ __forceinline__ int at(int r, int c) { return kRows >= 128 ? c * kRows + r : r * (kKvDim / 4) + c; }
+  // float4 c of row r: row after row, or (128 rows) column after column
+  static __device__ __forceinline__ int at(int r, int c) { return kRows == 128 ? c * kRows + r : r * (kKvDim / 4) + c; }
 };
 
 template <int kRows>

@@ -4,30 +4,25 @@
 // cores (sm_100a).  The mathematics, the sharing of the work and the join are
 // those of kvattn.cuh.
 //
-// A CTA works on one row tile at a time; where a request has more than 128 rows
-// (kPair), two CTAs work on a tile of 256, each on half the rows: the MMAs take a
-// K tile of which each CTA holds (and decodes) half the keys, and a V^T tile of which
-// each holds half the dims, so every code is decoded once for 256 rows
-// (cta_group::2; the first CTA issues them, the second one's warps report to its barriers).  Tensor memory: O [128 x 256] fp32 in
+// A CTA works on one row tile at a time.  Tensor memory: O [128 x 256] fp32 in
 // columns 0..255, the rotated rows Q [128 x 256] binary16 in 256..383, two score
 // tiles S [128 x 64] fp32 in 384..511, each overwritten by its P (binary16, 32
 // columns).  Q and P are the A operands (so shared memory carries only what is
 // decoded); K [64 keys][256 dims] and V^T [256 dims][64 keys] are the B operands,
 // both K-major with the 128-byte swizzle, decoded there from the 3-bit codes.
 //
-// Roles (19 warps):
+// Roles (18 warps):
 //   0..7   softmax: two threads per row (warps q and q + 4 of tensor-memory quarter
 //          q), half the columns each.  They put Q into tensor memory (rotated in
 //          two passes over the columns of O, which are free then), turn S(j) into
 //          P(j), rescale O when a row's reference rises (seldom, as in the few-row
 //          kernel; one reducing barrier of the two warps finds out), rotate O back
 //          and write the rows.
-//   8..15  decode (a pair's CTA: four warps K, four V): code pairs -> binary16 pairs through the 64-entry table (one
+//   8..15  decode: code pairs -> binary16 pairs through the 64-entry table (one
 //          copy per lane) -> 16-byte stores into the K and V^T tiles; window
 //          tiles are copied (K) and transposed (V) as they are, bf16.
-//   16, 17 issue the MMAs, one S(j), one O += P(j) V(j): a 64-column MMA takes three
-//          times as long to issue as to run, so the two products have a thread each.
-//   18     fetches codes and norms, 16 keys (never two pages) per bulk copy.
+//   16     issues the MMAs: S(j + 1), then O += P(j) V(j).
+//   17     fetches codes and norms, 16 keys (never two pages) per bulk copy.
 //
 // Keys stand in the tiles in an order that keeps every shared-memory access of
 // the decoders free of bank conflicts: row n = 8 w + g of the K tile is key
@@ -35,10 +30,15 @@
 // rows is the same key; P's columns follow by picking registers.  The 16-key
 // groups of a stage are 16 bytes further apart than their contents for the same reason.
 //
-// What bounds it: shared memory.  A single CTA's table reads, stores and staging
-// take about 1900 cycles of the SM's 128 bytes per cycle for a tile of 64 keys, the
-// MMAs' B operands 512 more, against 1024 cycles of matrix work (2800 cycles measured);
-// in a pair each CTA has half of that.
+// What bounds it, per tile of 64 keys (about 2900 cycles; the matrix work is 1024):
+// the softmax warps, busy for some 2500 cycles from S(j) to P(j) (tensor-memory
+// reads, norms, 8192 exponentials at 16 per cycle, packing), close to the decoders' 2250
+// and to shared memory, whose 128 bytes per cycle are busy four fifths of the time
+// (table reads and tile stores 1000 cycles, staging and norms 300, the MMAs' B
+// operands 512).  Tried and slower: four threads per row (1.07 times the time),
+// tiles taken in turn by two sets of softmax warps (1.2; the two S tiles that
+// tensor memory has room for then wait for each other), one issuing thread per product
+// (1.07), pairs of CTAs that decode half each for 256 rows (1.02 to 1.07).
 //
 // Every wait is bounded (wait_limit_ns from its own beginning), after which the
 // kernel raises HLWQ_DEVERR_TIMEOUT, drains its copies and MMAs and frees its
@@ -54,8 +54,8 @@ namespace hlwq {
 namespace {
 
 constexpr int kAtRows = 128;
-constexpr int kAtWarps = 19, kAtThreads = 32 * kAtWarps;
-constexpr int kAtDec0 = 8, kAtMma = 16, kAtPv = 17;
+constexpr int kAtWarps = 18, kAtThreads = 32 * kAtWarps;
+constexpr int kAtDec0 = 8, kAtMma = 16;
 constexpr int kAtWinUnit = 64;
 constexpr int kAtItemCost = 8;                       // units: an item takes about 12 us besides its tiles of 1.5 us
 constexpr int kGrp = 1536 + 16;                      // 16 keys' codes, and the gap
@@ -63,7 +63,7 @@ constexpr int kCodeStage = 12800;                    // K codes, V codes, norms 
 constexpr int kCodeStages = 3;
 constexpr int kNormOff = 2 * 4 * kGrp;               // 12416
 constexpr int kMaskOff = kNormOff + 256;
-constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile (a pair's CTA uses half)
+constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
 constexpr int kNrmSlot = 128 * 4 + 16;               // K norms, V norms, maxima of V's, mask
 constexpr float kMinQm = 1e-36f;                     // a zero scale: masked keys (-inf) stay masked, the others equal
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
@@ -77,34 +77,23 @@ __host__ __device__ constexpr int at_key(int n) {
   return 16 * (n & 3) + 2 * ((n >> 2) & 1) + ((n >> 3) & 1) + 4 * (n >> 4);
 }
 
-// Instruction descriptor: kind::f16 with binary16 or bfloat16 operands, K-major, D fp32,
-// M = 128 (256 for a pair).
-__host__ __device__ constexpr uint32_t idesc_16(int n, bool bf16, bool pair) {
-  return idesc_f16(n) + (pair ? static_cast<uint32_t>(128 >> 4) << 24 : 0u) + (bf16 ? (1u << 7) | (1u << 10) : 0u);
+// Instruction descriptor: kind::f16 with binary16 or bfloat16 operands, K-major, D fp32, M = 128.
+__host__ __device__ constexpr uint32_t idesc_16(int n, bool bf16) {
+  return idesc_f16(n) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Bounded wait whose limit starts when it has to wait; kCluster: for the other CTA's arrivals.
-template <bool kCluster = false>
+// Bounded wait whose limit starts when it has to wait.
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity) {
   uint64_t deadline = 0;
   for (uint32_t n = 1;; ++n) {
     uint32_t ok;
-    if constexpr (kCluster)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity)
-          : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
     if (ok) return true;
     if ((n & 63u) == 0u) {
       const uint64_t t = globaltimer_ns();
@@ -114,85 +103,43 @@ __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
-// A pair's second CTA reports to the first one's MMA issuers: one thread waits for
-// its own CTA's warps (cta scope, cheap for them) and passes it on at cluster scope,
-// once; with every warp arriving at cluster scope itself each tile waits
-// for the warps' own stores (1.2 times the time).
-__device__ __forceinline__ void report(uint32_t bar) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(r) : "memory");
-}
-
 // MMAs and commits are issued by one elected lane, but in warp-uniform control flow:
 // descriptors and addresses then stay in uniform registers.  Inside a branch of
-// one lane every MMA took about 90 cycles to issue.
-template <bool kPair>
+// one lane every MMA took about 90 cycles to issue, here 50.
 __device__ __forceinline__ void at_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-// The MMAs issued so far arrive at this barrier (of both CTAs) when they are done.
-template <bool kPair>
+// The MMAs issued so far arrive at this barrier when they are done.
 __device__ __forceinline__ void at_commit(uint32_t bar) {
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // The same for a whole warp: all lanes or none.
-template <bool kCluster = false>
 __device__ __forceinline__ bool at_wait_warp(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, at_wait<kCluster>(bar, parity));
+  return __all_sync(0xffffffffu, at_wait(bar, parity));
 }
 
 // No MMA may be under way when the tensor memory is freed: an issuing warp that
 // gives up waits for the ones it has issued, on a barrier of its own.
-template <bool kPair>
 __device__ __forceinline__ void drain_mma(uint32_t bar, int lane) {
   if (lane == 0) {
     mbar_init(bar, 1);
     fence_barrier_init();
   }
   __syncwarp();
-  if constexpr (kPair)
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-  else at_commit<false>(bar);
+  at_commit(bar);
   at_wait_warp(bar, 0);
 }
 
@@ -325,7 +272,6 @@ __device__ __forceinline__ void across_blocks(uint32_t row, int half, F&& f) {
   tc_wait_st();
 }
 
-template <bool kPair>
 __global__ void __launch_bounds__(kAtThreads, 1)
 kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut* __restrict__ cuts) {
   extern __shared__ __align__(16) uint8_t asm_raw[];
@@ -338,20 +284,16 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   const uint32_t nrm = codes + kCodeStages * kCodeStage, bars = nrm + 4 * kNrmSlot;
   const uint32_t c_full = bars, c_empty = c_full + 8 * kCodeStages, k_full = c_empty + 8 * kCodeStages, k_empty = k_full + 16,
                  v_full = k_empty + 16, v_empty = v_full + 16, s_full = v_empty + 16, p_full = s_full + 16,
-                 q_full = p_full + 16, k_peer = q_full + 8, vp_peer = k_peer + 16,
-                 q_peer = vp_peer + 16, misc = q_peer + 8;
+                 q_full = p_full + 16, misc = q_full + 8;
   volatile uint32_t* misc_g = reinterpret_cast<volatile uint32_t*>(g0 + (misc - tab0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kRows = kPair ? 2 * kAtRows : kAtRows, kHalf = kPair ? 2 : 1;
-  const int rank = kPair ? blockIdx.x & 1 : 0, me = blockIdx.x / kHalf;  // (clusters are consecutive CTAs)
-
-  if (threadIdx.x == 0 && rank == 0) cuts[me] = {0, 0, 0, 0};
+  if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
   int64_t mine0;
-  const int64_t U = kv_total_cost<kRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, warp_sums, mine0);
-  const KvShares share(U, me, gridDim.x / kHalf);
-  if (me >= share.ctas) return;  // (both of a pair) before any barrier or tensor memory
-  kv_find<kRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, mine0, share(me), found);
-  KvWalk<kRows, kAtWinUnit, kAtItemCost> w;
+  const int64_t U = kv_total_cost<kAtRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, warp_sums, mine0);
+  const KvShares share(U, blockIdx.x, gridDim.x);
+  if (share.i >= share.ctas) return;  // before any barrier or tensor memory
+  kv_find<kAtRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, mine0, share(share.i), found);
+  KvWalk<kAtRows, kAtWinUnit, kAtItemCost> w;
   w.begin(a, tiles, share, found);
 
   kv_check_codebook(a.codebook);
@@ -363,31 +305,22 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       mbar_init(c_empty + 8 * s, 8);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(k_full + 8 * s, 8 / kHalf);  // the decode warps that write it
+      mbar_init(k_full + 8 * s, 8);
       mbar_init(k_empty + 8 * s, 1);
-      mbar_init(v_full + 8 * s, 8 / kHalf);
+      mbar_init(v_full + 8 * s, 8);
       mbar_init(v_empty + 8 * s, 1);
       mbar_init(s_full + 8 * s, 1);
       mbar_init(p_full + 8 * s, 8);
-      mbar_init(k_peer + 8 * s, 1);          // the second CTA's reports
-      mbar_init(vp_peer + 8 * s, 1);
     }
-    mbar_init(q_peer, 1);
     mbar_init(q_full, 8);
     fence_barrier_init();
   }
   if (warp == kAtMma) {
-    if constexpr (kPair) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(misc), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // the barriers and the tensor memory of both are there
   tc_fence_after();
   const uint32_t tmem = misc_g[0];
   bool ok = true;
@@ -396,11 +329,11 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   // Ring slot and parity of tile j: j % 2 and (j / 2) & 1.
   if (warp < kAtDec0) {
     // ------------------------------------------------------------ softmax
-    const int half = warp >> 2, quarter = warp & 3, r0 = 32 * quarter + lane, r = kAtRows * rank + r0;  // r: row of the tile
+    const int half = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;  // r: row of the tile
     const uint32_t row = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float sgn = a.scale < 0.0f ? -1.0f : 1.0f;
-    float* mine = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + half * kAtRows + r0;       // exchange with the
-    const float* other = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + (half ^ 1) * kAtRows + r0;  // row's other thread
+    float* mine = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + half * kAtRows + r;       // exchange with the
+    const float* other = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + (half ^ 1) * kAtRows + r;  // row's other thread
     uint32_t gt = 0;
     // the product of tile j has been added to O (tile j - 2's was before S(j) came)
     auto pv_done = [&](uint32_t j) { return at_wait_warp(v_empty + 8 * (j & 1u), (j >> 1) & 1u); };
@@ -410,9 +343,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       const int tr = it.row0 + (on ? r : 0), tok = tr / a.G, head = w.h * a.G + (tr - tok * a.G);
       const uint16_t* qrow = a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + head * kKvDim;
       const int lim = on ? it.p + tok + 1 : 0;
-      if (threadIdx.x == 0 && rank == 0) {
+      if (threadIdx.x == 0) {
         KvCut cut;
-        if (w.note(share, cut)) cuts[me] = cut;
+        if (w.note(share, cut)) cuts[blockIdx.x] = cut;
       }
       // m: the row's reference; lf: log2 of the power of two that keeps p n in
       // binary16's range, in l as in O; l: this thread's share of the row's sum
@@ -650,7 +583,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       const bool whole = w.ta == 0 && w.tb == it.units;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       uint16_t* orow = a.out + static_cast<int64_t>(it.c0 + tok) * a.ldo + head * kKvDim;
-      float* part = parts + static_cast<int64_t>(2 * me + (w.ta == 0 ? 1 : 0)) * (kRows * (kKvDim + 2));
+      float* part = parts + static_cast<int64_t>(2 * blockIdx.x + (w.ta == 0 ? 1 : 0)) * (kAtRows * (kKvDim + 2));
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 16) {
         uint32_t x[16];
@@ -668,29 +601,25 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         } else if (on) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // [256 columns / 4][row][4]: a warp writes 512 bytes at a time
-            reinterpret_cast<uint4*>(part)[(c / 4 + k) * kRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            reinterpret_cast<uint4*>(part)[(c / 4 + k) * kAtRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
         __syncwarp();
       }
       if (!whole && on && half == 0) {
-        part[kRows * kKvDim + r] = m;
-        part[kRows * (kKvDim + 1) + r] = l;
+        part[kAtRows * kKvDim + r] = m;
+        part[kAtRows * (kKvDim + 1) + r] = l;
       }
       pair_sync(quarter);  // O, Q and the exchange words are free for the next segment
     }
   } else if (warp < kAtMma) {
     // ------------------------------------------------------------ decode
-    // dl: this warp's place among those that decode K, or V, in this CTA; dw: in the whole tile
-    const int g = lane & 7, t4 = lane >> 3, tid = threadIdx.x - 32 * kAtDec0;
-    const bool do_k = !kPair || warp < kAtDec0 + 4, do_v = !kPair || !do_k;
-    const int dl = kPair ? (warp - kAtDec0) & 3 : warp - kAtDec0, dw = dl + 4 * rank;
-    constexpr int kSlab = 8192 / kHalf;  // K tile: rows x 64 dims
+    const int dw = warp - kAtDec0, g = lane & 7, t4 = lane >> 3, tid = threadIdx.x - 32 * kAtDec0;
     const uint32_t tab = tab0 + 4 * lane;
     uint32_t gt = 0, ce = 0;
     while (ok && w.next(a, tiles)) {
       for (int t = w.ta; ok && t < w.e_tb; ++t, ++gt, ++ce) {
         const uint32_t cs = ce % kCodeStages, st = codes + cs * kCodeStage, s = gt & 1u, par = (gt >> 1) & 1u;
-        ok = at_wait_warp(c_full + 8 * cs, (ce / kCodeStages) & 1u) && (!do_k || at_wait_warp(k_empty + 8 * s, par ^ 1u));
+        ok = at_wait_warp(c_full + 8 * cs, (ce / kCodeStages) & 1u) && at_wait_warp(k_empty + 8 * s, par ^ 1u);
         if (!ok) break;
         const uint32_t there = lds32(st + kMaskOff);
         const int left = w.it.e_lim - t * kUnit;  // keys from here to the end
@@ -705,7 +634,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           if (tid >= 64 && lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 512 + 4 * ((tid - 64) >> 5)), "r"(mx) : "memory");
           if (tid == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 520), "r"(there) : "memory");
         }
-        if (do_k) {  // K: key of row 8 dw + g, dims 64 t4 .. + 63
+        {  // K: key of row 8 dw + g, dims 64 t4 .. + 63
           const uint32_t src = st + (g & 3) * kGrp + (2 * (g >> 2) + (dw & 1) + 4 * (dw >> 1)) * kKvBytes + 24 * t4;
           uint32_t x[6];
 #pragma unroll
@@ -713,7 +642,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             const uint2 y = lds64(src + 8 * i);
             x[2 * i] = y.x, x[2 * i + 1] = y.y;
           }
-          const uint32_t dst = k_tiles + s * kKvTile + kSlab * t4 + (8 * dl + g) * 128;
+          const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t h[4];
@@ -732,10 +661,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           __syncwarp();
           if (lane == 0) mbar_arrive(k_full + 8 * s);
         }
-        if (do_v) {
-          ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
-          if (!ok) break;
-          // V^T: places 8 g .. + 7, dims 8 (4 dw + t4) .. + 7: 24 bits of each of eight keys
+        ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        {  // V^T: places 8 g .. + 7, dims 8 (4 dw + t4) .. + 7: 24 bits of each of eight keys
           const uint32_t src = st + 4 * kGrp + (g & 3) * kGrp + 2 * (g >> 2) * kKvBytes + 12 * dw + 4 * ((24 * t4) >> 5);
           uint32_t x[8];
 #pragma unroll
@@ -743,7 +671,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             const uint32_t at = src + ((i & 1) + 4 * (i >> 1)) * kKvBytes;
             x[i] = __funnelshift_r(lds32(at), lds32(at + 4), (24 * t4) & 31);
           }
-          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dl + t4) * 128;
+          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
           constexpr uint32_t kEven = 0x1c71c7u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // even and odd codes of two keys side by side
@@ -774,12 +702,12 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       for (int t = w.e_tb; ok && t < w.tb; ++t, ++gt) {
         const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
         const int k0 = w.it.e_lim + (t - w.it.e_units) * kAtWinUnit, end = w.it.w_lim;
-        if (do_k) {
-          ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
-          if (!ok) break;
+        ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        {
           const int key = k0 + at_key(8 * dw + g);
           const uint4* src = reinterpret_cast<const uint4*>(a.kwin + (ring + (key < end ? key % R : 0)) * kKvDim + 64 * t4);
-          const uint32_t dst = k_tiles + s * kKvTile + kSlab * t4 + (8 * dl + g) * 128;
+          const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -790,9 +718,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           __syncwarp();
           if (lane == 0) mbar_arrive(k_full + 8 * s);
         }
-        if (do_v) {
-          ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
-          if (!ok) break;
+        ok = at_wait_warp(v_empty + 8 * s, par ^ 1u);
+        if (!ok) break;
+        {
           uint32_t x[8][4];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -801,7 +729,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             if (key < end) y = __ldg(reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 8 * (4 * dw + t4)));
             x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
           }
-          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dl + t4) * 128;
+          const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t h[4];
@@ -817,85 +745,63 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     }
     if (ok) {  // the last commits' arrivals land before the CTA ends
       const uint32_t s = (gt - 1) & 1u, par = ((gt - 1) >> 1) & 1u;
-      ok = (!do_k || at_wait_warp(k_empty + 8 * s, par)) && (!do_v || at_wait_warp(v_empty + 8 * s, par));
+      ok = at_wait_warp(k_empty + 8 * s, par) && at_wait_warp(v_empty + 8 * s, par);
     }
   } else if (warp == kAtMma) {
-    // ------------------------------------------------------------ MMA issuer: S
-    // (in a pair's second CTA these loops pass its readiness on to the first one)
-    {
-      uint32_t gt = 0, nq = 0;
-      while (ok && w.next(a, tiles)) {
-        for (int phase = 0; ok && phase < 2; ++phase) {
-          const bool win = phase == 1;
-          const int n = win ? w.tb - w.e_tb : w.e_tb - w.ta;
-          if (n == 0) continue;
-          ok = at_wait_warp(q_full, nq & 1u);
-          if (ok && kPair) {
-            if (rank) {
-              tc_fence_after();
-              tc_fence_before();
-              if (lane == 0) report(q_peer);
-            }
-            else ok = at_wait_warp<true>(q_peer, nq & 1u);
-          }
-          ++nq;
-          const uint32_t id = idesc_16(64, win, kPair);
-          for (int t = 0; ok && t < n; ++t, ++gt) {
-            const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
-            // S(gt)'s columns were P(gt - 2): v_empty says that its product is done
-            ok = at_wait_warp(k_full + 8 * s, par);
-            if (ok && rank) {
-              if (lane == 0) report(k_peer + 8 * s);
-              continue;
-            }
-            ok = ok && at_wait_warp(v_empty + 8 * s, par ^ 1u) && (!kPair || at_wait_warp<true>(k_peer + 8 * s, par));
-            if (!ok) break;
-            tc_fence_after();
+    // ------------------------------------------------------------ MMA issuer
+    uint32_t gt = 0, nq = 0;
+    // O (+)= P(j) V(j)
+    auto pv = [&](uint32_t j, bool win, bool first) -> bool {
+      const uint32_t s = j & 1u, par = (j >> 1) & 1u;
+      if (!at_wait_warp(v_full + 8 * s, par) || !at_wait_warp(p_full + 8 * s, par)) return false;
+      tc_fence_after();
+      const uint64_t desc = smem_desc_sw128(v_tiles + s * kKvTile);
+      const uint32_t id = idesc_16(256, win);
+      for (int part = 0; part < (win ? 2 : 1); ++part)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint64_t desc = smem_desc_sw128(k_tiles + s * kKvTile + 8192 / kHalf * c);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                at_mma<kPair>(tmem + kColS + 64 * s, tmem + kColQ + 32 * c + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
-                              c || k ? 1u : 0u);
-            }
-            at_commit<kPair>(k_empty + 8 * s);
-            at_commit<kPair>(s_full + 8 * s);
-          }
-        }
-      }
-      if (!ok && rank == 0) drain_mma<kPair>(misc + 16, lane);
-    }
-  } else if (warp == kAtPv) {
-    // ------------------------------------------------------------ MMA issuer: O += P V
-    {
-      uint32_t gt = 0;
-      while (ok && w.next(a, tiles)) {
-        const int ne = w.e_tb - w.ta, n = w.tb - w.ta;
+        for (int k = 0; k < 4; ++k)
+          at_mma(tmem + kColO, tmem + kColS + 64 * s + 32 * part + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
+                        first && part == 0 && k == 0 ? 0u : 1u);
+      at_commit(v_empty + 8 * s);
+      return true;
+    };
+    while (ok && w.next(a, tiles)) {
+      bool first = true;
+      for (int phase = 0; ok && phase < 2; ++phase) {
+        const bool win = phase == 1;
+        const int n = win ? w.tb - w.e_tb : w.e_tb - w.ta;
+        if (n == 0) continue;
+        ok = at_wait_warp(q_full, nq & 1u);
+        ++nq;
+        const uint32_t id = idesc_16(64, win);
         for (int t = 0; ok && t < n; ++t, ++gt) {
-          const bool win = t >= ne;
-          const uint32_t s = gt & 1u, par = (gt >> 1) & 1u, id = idesc_16(256, win, kPair);
-          ok = at_wait_warp(v_full + 8 * s, par) && at_wait_warp(p_full + 8 * s, par);
-          if (ok && rank) {
-            tc_fence_after();
-            tc_fence_before();
-            if (lane == 0) report(vp_peer + 8 * s);
-            continue;
-          }
-          ok = ok && (!kPair || at_wait_warp<true>(vp_peer + 8 * s, par));
+          const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
+          ok = at_wait_warp(k_full + 8 * s, par);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t desc = smem_desc_sw128(v_tiles + s * kKvTile);
-          for (int part = 0; part < (win ? 2 : 1); ++part)
+          // S(gt)'s columns were P(gt - 2): its product was issued before, and MMAs run in order
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint64_t desc = smem_desc_sw128(k_tiles + s * kKvTile + 8192 * c);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              at_mma<kPair>(tmem + kColO, tmem + kColS + 64 * s + 32 * part + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
-                            t == 0 && part == 0 && k == 0 ? 0u : 1u);
-          at_commit<kPair>(v_empty + 8 * s);
+              at_mma(tmem + kColS + 64 * s, tmem + kColQ + 32 * c + 8 * k, desc + static_cast<uint64_t>(2 * k), id,
+                            c || k ? 1u : 0u);
+          }
+          at_commit(k_empty + 8 * s);
+          at_commit(s_full + 8 * s);
+          if (t > 0) {
+            ok = pv(gt - 1, win, first);
+            first = false;
+          }
+        }
+        if (ok) {
+          ok = pv(gt - 1, win, first);
+          first = false;
         }
       }
-      if (!ok && rank == 0) drain_mma<kPair>(misc + 24, lane);
     }
+    if (!ok) drain_mma(misc + 16, lane);
   } else {
     // ------------------------------------------------------------ loader
     uint32_t ce = 0;
@@ -943,58 +849,42 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // no arrival and no MMA of the other CTA is under way
   if (warp == kAtMma) {
     tc_fence_after();
-    if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
-    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 
-template <bool kPair>
-int launch_tiles(const KvAttn& a, int shares, int tiles, float* parts, KvCut* cuts, cudaStream_t stream) {
+int launch_tiles(const KvAttn& a, int ctas, int tiles, float* parts, KvCut* cuts, cudaStream_t stream) {
   static PerDeviceOnce attr;
   if (const int st = attr([&] {
-        return cudaFuncSetAttribute(kv_attn_tile_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem) ==
+        return cudaFuncSetAttribute(kv_attn_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAtSmem) ==
                cudaSuccess;
       }))
     return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(shares * (kPair ? 2 : 1));
-  cfg.blockDim = dim3(kAtThreads);
-  cfg.dynamicSmemBytes = kAtSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = kPair ? 2 : 1;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = kPair ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kv_attn_tile_kernel<kPair>, a, tiles, parts, cuts) != cudaSuccess) return HLWQ_ECUDA;
-  return launch_join<kPair ? 2 * kAtRows : kAtRows>(a, shares, parts, cuts, stream);
+  kv_attn_tile_kernel<<<ctas, kAtThreads, kAtSmem, stream>>>(a, tiles, parts, cuts);
+  if (cudaGetLastError() != cudaSuccess) return HLWQ_ECUDA;
+  return launch_join<kAtRows>(a, ctas, parts, cuts, stream);
 }
 
-// Rows per tile, CTAs (or pairs) that share the work, and row tiles of a request,
-// for max_new new tokens: the few-row kernel up to 16 rows per kv head, above
-// it the tensor-core tiles, in pairs where a request has more than one tile of 128.
+// Rows per tile, CTAs, and row tiles of a request for max_new new tokens: the
+// few-row kernel up to 16 rows per kv head, the tensor-core tiles above.
 struct KvGrid {
-  int rows, shares;
+  int rows, ctas;
   int64_t tiles;
 };
 inline KvGrid kv_grid(int64_t max_new, int64_t G) {
   const int64_t n = max_new * G;
-  const int rows = n <= 8 ? 8 : n <= 16 ? 16 : n <= kAtRows ? kAtRows : 2 * kAtRows;
-  const int sms = sm_count();
-  return {rows, rows == 8 ? sms * RowCfg<1>::kCtas : rows == 16 ? sms * RowCfg<2>::kCtas : rows == kAtRows ? sms : sms / 2,
-          ceil_div(n, rows)};
+  const int rows = n <= 8 ? 8 : n <= 16 ? 16 : kAtRows;
+  return {rows, sm_count() * (rows == 8 ? RowCfg<1>::kCtas : rows == 16 ? RowCfg<2>::kCtas : 1), ceil_div(n, rows)};
 }
 
 }  // namespace
 
-// Workspace: two partial results per share, then a note per share for the join.
+// Workspace: two partial results per CTA, then a note per CTA for the join.
 size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t Hq, int64_t H) {
   const KvGrid gr = kv_grid(max_new, Hq / H);
-  return static_cast<size_t>(gr.shares) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
+  return static_cast<size_t>(gr.ctas) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
 }
 
 int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
@@ -1002,12 +892,11 @@ int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_
   if (gr.tiles * a.B > INT32_MAX) return HLWQ_EUNSUPPORTED;
   const int tiles = static_cast<int>(gr.tiles);
   float* parts = static_cast<float*>(workspace);
-  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.shares * gr.rows * (kKvDim + 2));
+  KvCut* cuts = reinterpret_cast<KvCut*>(parts + static_cast<int64_t>(2) * gr.ctas * gr.rows * (kKvDim + 2));
   switch (gr.rows) {
-    case 8: return launch_rows<1>(a, gr.shares, tiles, parts, cuts, stream);
-    case 16: return launch_rows<2>(a, gr.shares, tiles, parts, cuts, stream);
-    case kAtRows: return launch_tiles<false>(a, gr.shares, tiles, parts, cuts, stream);
-    default: return launch_tiles<true>(a, gr.shares, tiles, parts, cuts, stream);
+    case 8: return launch_rows<1>(a, gr.ctas, tiles, parts, cuts, stream);
+    case 16: return launch_rows<2>(a, gr.ctas, tiles, parts, cuts, stream);
+    default: return launch_tiles(a, gr.ctas, tiles, parts, cuts, stream);
   }
 }
 
