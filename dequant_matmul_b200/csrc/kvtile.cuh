@@ -382,7 +382,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         }
         const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + 520);  // 16-key groups whose page is there
         const int see = min(lim, end) - k0;
-        if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
+        const bool masked = __any_sync(0xffffffffu, see < 64) || there != 15u;
+        if (masked) {
           const int sh = see - 2 * half;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -452,7 +453,13 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         if constexpr (!kWin) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float4 x = lds_f4(nb + 256 + 32 * i);
+            float4 x = lds_f4(nb + 256 + 32 * i);
+            if (masked) {  // a key that is masked out has no say, whatever its norm is
+              if (v[i][0].x == 0.0f) x.x = 0.0f;
+              if (v[i][0].y == 0.0f) x.y = 0.0f;
+              if (v[i][1].x == 0.0f) x.z = 0.0f;
+              if (v[i][1].y == 0.0f) x.w = 0.0f;
+            }
             v[i][0] = mul2(v[i][0], make_float2(x.x, x.y));
             v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
           }

@@ -258,9 +258,11 @@ def test_attention(hl, cb8, past, new, H, G, P, R):
     out = hl.kv_paged_attention(*args, **kw)
     torch.cuda.synchronize()
     _check(out, want, tol, sum(new))
-    again = hl.kv_paged_attention(*args, scale=kw["scale"], out=torch.full_like(out, 7.0))
+    # the same inputs give the same bits, whatever the workspace held
+    ws = torch.full((hl.kv_attention_workspace(args[0], H, len(past), max(new)),), 255, dtype=torch.uint8, device="cuda")
+    again = hl.kv_paged_attention(*args, scale=kw["scale"], out=torch.full_like(out, 7.0), workspace=ws)
     torch.cuda.synchronize()
-    assert torch.equal(out, again)     # the same inputs give the same bits
+    assert torch.equal(out, again)
     assert hl.device_error() == 0
 
 
@@ -376,6 +378,80 @@ def test_attention_nan_stays_in_its_row(hl, cb8):
         assert torch.all(torch.isnan(out[1, 2]))
         out[1, 2] = torch.from_numpy(want[1, 2]).to(out.dtype).cuda()
         _check(out, want, tol, new[0])
+
+
+@pytest.mark.parametrize("new", [3, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attention_tokens_ahead_have_no_say(hl, cb8, new, value):
+    """Norms that are not finite, of tokens that a query does not see."""
+    args, kw, want, tol = _attend(hl, cb8, [70], [new], 1, 4, 16, 0, seed=12)
+    page, at = int(args[3][0, (70 + new - 1) // 16]), (70 + new - 1) % 16
+    for norms in (args[4][1], args[5][1]):
+        norms.view(torch.float16)[page, 0, at] = value
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    if value != value:   # the last token itself sees it (an infinite norm may give a score of -inf, which has no weight)
+        assert not torch.any(torch.isfinite(out[new - 1]))
+    out[new - 1] = torch.from_numpy(want[new - 1]).to(out.dtype).cuda()
+    _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("new", [1, 2, 60])
+def test_attention_long_items_are_cut_and_joined(hl, cb8, new):
+    """One request, one kv head: every CTA gets a part of the same rows."""
+    args, kw, want, tol = _attend(hl, cb8, [5000], [new], 1, 8, 64, 100, seed=5)
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    _check(out, want, tol, new)
+
+
+def test_attention_many_requests(hl, cb8):
+    """More requests than CTAs, most of them without tokens."""
+    rng = np.random.default_rng(0)
+    past, new = [int(x) for x in rng.integers(0, 60, 700)], [0] * 700
+    for b in rng.choice(700, 90, replace=False):
+        new[b] = 1
+    args, kw, want, tol = _attend(hl, cb8, past, new, 1, 2, 16, 8, seed=1)
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    _check(out, want, tol, 90)
+
+
+def test_attention_wait_runs_out(hl, cb8):
+    """The tile kernel whose code copies never come (failure-detection build, waits of
+    5 ms): the status says so, the tensor memory is given back, the next call is right."""
+    args, kw, want, tol = _attend(hl, cb8, [100, 30], [40, 50], 2, 4, 16, 8, seed=7)
+    prod = hl.lib
+    hl.lib = hl.load_library(hl.FAULT_LIB_PATH)
+    try:
+        hl.device_error()
+        assert hl.lib.hlwq_fault_inject(1, 5_000_000) == hl.HLWQ_OK
+        hl.kv_paged_attention(*args, **kw)
+        assert hl.device_error() & hl.DEVERR_TIMEOUT
+        assert hl.lib.hlwq_fault_inject(0, 2_000_000_000) == hl.HLWQ_OK
+        out = hl.kv_paged_attention(*args, scale=None, out=torch.full_like(kw["out"], 7.0))
+        torch.cuda.synchronize()
+        assert hl.device_error() == 0
+    finally:
+        hl.lib.hlwq_fault_inject(0, 2_000_000_000)
+        hl.lib = prod
+    _check(out, want, tol, 90)
+
+
+def test_two_streams_at_once(hl, cb8):
+    """Two batches on two streams, each with its own workspace."""
+    runs = [_attend(hl, cb8, p, n, 2, 6, 64, 128, seed=s) for s, (p, n) in enumerate([([900, 300], [1, 1]), ([200], [150])])]
+    side = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        outs = []
+        for (args, kw, _, _), st in zip(runs, side):
+            with torch.cuda.stream(st):
+                outs.append(hl.kv_paged_attention(*args, scale=None, out=torch.full_like(kw["out"], 7.0)))
+    torch.cuda.synchronize()
+    for out, (args, kw, want, tol) in zip(outs, runs):
+        _check(out, want, tol, want.shape[0])
 
 
 # ------------------------------------------------------------------ together
