@@ -382,8 +382,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         }
         const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + 520);  // 16-key groups whose page is there
         const int see = min(lim, end) - k0;
-        const bool masked = __any_sync(0xffffffffu, see < 64) || there != 15u;
-        if (masked) {
+        if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
           const int sh = see - 2 * half;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -453,13 +452,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         if constexpr (!kWin) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float4 x = lds_f4(nb + 256 + 32 * i);
-            if (masked) {  // a key that is masked out has no say, whatever its norm is
-              if (v[i][0].x == 0.0f) x.x = 0.0f;
-              if (v[i][0].y == 0.0f) x.y = 0.0f;
-              if (v[i][1].x == 0.0f) x.z = 0.0f;
-              if (v[i][1].y == 0.0f) x.w = 0.0f;
-            }
+            const float4 x = lds_f4(nb + 256 + 32 * i);
             v[i][0] = mul2(v[i][0], make_float2(x.x, x.y));
             v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
           }
@@ -632,8 +625,10 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         const int left = w.it.e_lim - t * kUnit;  // keys from here to the end
         if (tid < 128) {
           const int n = tid & 63, key = at_key(n);
-          const uint32_t wd = lds32(st + kNormOff + (tid >> 6) * 128 + 4 * (key >> 1));
-          float x = half_bits_to_float(static_cast<uint16_t>(wd >> (16 * (key & 1))));
+          const float nk = lds_half(st + kNormOff + 2 * key), nv = lds_half(st + kNormOff + 128 + 2 * key);
+          // A value's norm that is not finite goes into its key's: the rows that see it
+          // come out NaN, and 0 * inf does not reach those that do not.
+          float x = tid < 64 ? (isfinite(nv) ? nk : NAN) : (isfinite(nv) ? nv : 0.0f);
           if (key >= left || !((there >> (key >> 4)) & 1u)) x = 0.0f;
           const uint32_t slot = nrm + (gt & 3u) * kNrmSlot;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + 4 * tid), "f"(x) : "memory");
