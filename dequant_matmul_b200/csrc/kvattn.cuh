@@ -1,13 +1,15 @@
 #pragma once
-// Attention of new tokens over the paged Q3 KV cache (sm_100a).
+// Attention of new tokens over the paged Q3 KV cache (sm_100a): the sharing of the
+// work, the kernel for few rows per kv head, the join of split results.  The
+// kernel for chunks is kvtile.cuh.
 //
 // Query i of a request with p cached and n new tokens sees keys j <= p + i:
 //   s_j = scale * q . k_j,  o = sum_j softmax(s)_j v_j,
 // keys and values below n_enc(p + n) decoded from their pages, the rest exact
-// from the window.  Everything runs in the rotated domain: with H = H256
-// (symmetric, H H = 256 I), q . k = (q H) . (c[code] n / 256) for an encoded
-// key and (q H) . (k H) / 256 for a window key, and o = (1/256) (sum_j p_j y_j) H
-// with y_j = n_j c[code_j] / 1 or v_j H: no cached vector is ever un-rotated.
+// from the window.  With H = H256 (symmetric, H H = 256 I), an encoded key is
+// n / 256 c[code] H: q . k = (n / 256) (q H) . c[code], and the encoded values add up to
+// (1 / 256) (sum_j p_j n_j c[code_j]) H.  The query is rotated once, the sum once,
+// and the cached vectors never; what is multiplied are the 8 centroids.
 
 #include "kvpage.cuh"
 #include "sm100.cuh"
@@ -346,14 +348,23 @@ __device__ __forceinline__ void cp_async_wait() {
 //
 // P^T comes out of S^T's registers by two 8 x 8 transposes; row sums
 // stay in the lane until the end.  The running reference of a row's maximum is
-// raised only when a score exceeds it by 2^8 (exp2 stays below 2^8): the
+// raised only when a score exceeds it by 8 (in powers of two; p stays below 2^8): the
 // sums are the same, most steps need no exchange between lanes.  A value's norm
 // rides on p; p n is kept in binary16's range by a power of two that follows the
-// largest norm (fv), so neither overflows and what is lost is 2^-39 of the
-// largest.  O^T's registers hold 32 consecutive dims of two rows: the
+// largest norm (fv), so it does not overflow and what is lost is below 2^-29 of the
+// largest term.  O^T's registers hold 32 consecutive dims of two rows: the
 // rotation back is five in-register and three shuffle stages.  The window's keys
 // come after it and are multiplied as they are, un-rotated bf16 with the query's
 // own bits.
+//
+// Bound: HBM by its bytes (196 per token and kv head); in fact integer instructions
+// and shared-memory reads, one warp instruction in five a table read.  64 requests
+// of 64 to 16384 tokens, 4 kv heads of 6 rows (438 MB): 166 us, 2.6 TB/s, DRAM
+// traffic equal to the bytes, 730 warp instructions per 16 keys at 2.3 per cycle
+// (ALU pipe 57 %, shared memory 57 %).  A tcgen05 kernel would have to write the decoded
+// tiles to shared memory first, as much traffic again as the table reads; the
+// legacy instruction takes them from registers, and with 8 or 16 rows its
+// rate is no limit (tensor pipe 20 %).
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
