@@ -431,6 +431,15 @@ def _pool(k_pages, v_pages, window, B: int, dev: int):
             _array(window[1], "window[1]", torch.bfloat16, shape, dev), n, h, p, R)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one): taken from that
+    stream's memory, so that nothing else uses it before the call or after it is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _launch(what: str, fn, dev: int, stream, *args):
     """Calls a library function whose last argument is the stream, on the tensors'
     device and (by default) its current stream."""
@@ -455,13 +464,13 @@ def kv_block_tables(n_past, n_new, free_pages, n_free, block_table, page_size: i
     if slot_map is None:
         if T is None:
             raise HLWQError("kv_block_tables needs T or slot_map")
-        slot_map = torch.empty(T, dtype=torch.int64, device=n_past.device)
+        slot_map = _empty(T, torch.int64, n_past.device, stream)
     elif T is None:
         T = slot_map.numel()
     if n_free_out is None:
-        n_free_out = torch.empty(1, dtype=i32, device=n_past.device)
+        n_free_out = _empty(1, i32, n_past.device, stream)
     if cu_new is None:
-        cu_new = torch.empty(B + 1, dtype=i32, device=n_past.device)
+        cu_new = _empty(B + 1, i32, n_past.device, stream)
     cap = free_pages.numel()
     if block_table.dim() != 2:
         raise HLWQError(f"block_table must be [B][max_pages], not {list(block_table.shape)}")
@@ -513,7 +522,7 @@ def kv_paged_attention(Q, cu_new, n_past, block_table, k_pages, v_pages, window,
     if H == 0 or Hq % H:
         raise HLWQError(f"{Hq} query heads are not a multiple of {H} kv heads")
     if out is None:
-        out = torch.empty(T, Hq, 256, dtype=torch.bfloat16, device=Q.device)
+        out = _empty((T, Hq, 256), torch.bfloat16, Q.device, stream)
     elif out.shape != Q.shape:
         raise HLWQError(f"out must be {list(Q.shape)}, not {list(out.shape)}")
     if block_table.dim() != 2:
@@ -525,7 +534,7 @@ def kv_paged_attention(Q, cu_new, n_past, block_table, k_pages, v_pages, window,
                 need = kv_attention_workspace(Q, H, B, max_new)
         else:
             need = kv_attention_workspace(Q, H, B, max_new)
-        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        workspace = _empty(need, torch.uint8, Q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise HLWQError(f"workspace must be contiguous and on cuda:{dev}")
     _launch("hlwq_kv_paged_attention", lib.hlwq_kv_paged_attention, dev, stream, Q.data_ptr(), ldq, T, Hq, H,

@@ -454,6 +454,25 @@ def test_two_streams_at_once(hl, cb8):
         _check(out, want, tol, want.shape[0])
 
 
+def test_a_step_on_a_given_stream(hl, cb8):
+    """stream=...: the step waits for nothing of the current stream, and what it
+    allocates itself is not handed to the current stream's work meanwhile."""
+    H, G, T = 2, 4, 60
+    K, V, Q = _rows(T, H, 1).cuda(), _rows(T, H, 2).cuda(), _rows(T, H * G, 3, False).cuda()
+    cache = hl.PagedKVCache(1, H, num_pages=8, max_pages=8, page_size=16, R=16, cb8=cb8)
+    n_new, side = _ints([T]), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    cache.begin(n_new, T, stream=side)
+    cache.append(K, V, stream=side)
+    out = cache.attention(Q, T, stream=side)
+    cache.end(stream=side)
+    noise = [torch.full((1 << 18,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    want, tol = _reference(K.cpu(), V.cpu(), Q.cpu(), T, T, 16, G)
+    _check(out, want, tol, T)
+    assert len(noise) == 64 and cache.n_past.tolist() == [T]
+
+
 # ------------------------------------------------------------------ together
 def _reference(X, Y, Q, N, n, R, G):
     """The last n queries of one request's N tokens, heads [N][H][256]."""
