@@ -603,11 +603,13 @@ class PagedKVCache:
             self.n_free.copy_(self._n_free_next)
 
     def release(self, b: int):
-        """Empties request row b and gives its pages back (reads its length: synchronises)."""
+        """Empties request row b between two steps and gives its pages back
+        (reads its length: synchronises)."""
         k = -(-max(0, int(self.n_past[b]) - self.R) // self.page_size)
-        k = min(k, self.block_table.shape[1])
-        n = int(self.n_free)
-        self.free_pages[n:n + k] = self.block_table[b, :k]
+        pages = self.block_table[b, :k]
+        pages = pages[pages >= 0]  # an exhausted pool leaves -1 in the table
+        n, k = int(self.n_free), pages.numel()
+        self.free_pages[n:n + k] = pages
         self.n_free += k
         self.block_table[b] = -1
         self.n_past[b] = 0

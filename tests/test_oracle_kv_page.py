@@ -168,3 +168,19 @@ def test_binding_refuses_before_it_calls(hl):
         hl.kv_paged_append(x, x, i.long(), i, i[:4], None, None, None, None)
     with pytest.raises(hl.HLWQError, match="CUDA"):
         hl.kv_paged_attention(x, i, i[:4], None, None, None, None, None, 1)
+
+
+def test_release_gives_back_the_pages_that_there_are(hl):
+    """Row 0 has 5 pages' tokens, but the pool ran out behind the third page."""
+    cache = hl.PagedKVCache(2, 1, 8, 6, page_size=16, R=4, device="cpu", cb8=torch.zeros(8))
+    cache.block_table[0, :5] = torch.tensor([7, 2, 6, -1, -1], dtype=torch.int32)
+    cache.block_table[1, :1] = 5
+    cache.n_past[:] = torch.tensor([4 + 70, 4 + 3], dtype=torch.int32)
+    cache.n_free[0] = 4                                      # pages 0, 1, 3, 4
+    cache.free_pages[:4] = torch.tensor([0, 1, 3, 4], dtype=torch.int32)
+    cache.release(0)
+    assert int(cache.n_free) == 7 and cache.free_pages[:7].tolist() == [0, 1, 3, 4, 7, 2, 6]
+    assert cache.block_table[0].tolist() == [-1] * 6 and cache.n_past.tolist() == [0, 7]
+    cache.release(0)                                         # an empty row
+    cache.release(1)
+    assert int(cache.n_free) == 8 and sorted(cache.free_pages.tolist()) == list(range(8))
