@@ -294,6 +294,9 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Of two bf16 values, the sign bits of those that are not finite (exponent all ones).
+__device__ __forceinline__ uint32_t not_finite_bf162(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -740,7 +743,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     }
 
     // ---- window keys, 16 at a time and as they are: bf16 operands, scores exact to
-    // fp32, p in two bf16 parts (16 bits)
+    // fp32, p in two bf16 parts (16 bits).  In a tile that some rows see in part, a value
+    // that is not finite is carried by its key's score: the rows that see it come out
+    // NaN, and 0 * inf does not reach those that do not.
     const int w_first = it.e_lim + (max(ta, it.e_units) - it.e_units) * kRowWinUnit;
     const int w_end = min(it.e_lim + (tb - it.e_units) * kRowWinUnit, it.w_lim);
     if (w_first < w_end) {
@@ -751,6 +756,19 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {
       const int R = static_cast<int>(a.R);
       const int64_t ring = (static_cast<int64_t>(it.b) * a.H + h) * R;
+      uint32_t bad = 0;  // bits 2 i, 2 i + 1: halves of key i's value
+      if (min(k0 + 16, w_end) > it.p + it.row0 / a.G + 1) {
+        const int key = k0 + (lane >> 1);
+        if (key < w_end) {
+          const uint4* src = reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 128 * (lane & 1));
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 x = __ldg(src + c);
+            bad |= not_finite_bf162(x.x) | not_finite_bf162(x.y) | not_finite_bf162(x.z) | not_finite_bf162(x.w);
+          }
+        }
+        bad = __ballot_sync(0xffffffffu, bad != 0u);
+      }
       float d[1][NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) d[0][nt][0] = d[0][nt][1] = d[0][nt][2] = d[0][nt][3] = 0.0f;
@@ -772,6 +790,13 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
         }
       }
+      if (bad) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((bad >> (2 * g + 16 * (k >> 1))) & 3u) d[0][nt][k] = NAN;
+      }
       const float one[1][2] = {{1.0f, 1.0f}};
       const int key[1] = {k0 + g}, end[1] = {w_end};
       score(d, one, key, end);
@@ -788,8 +813,8 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       bool on[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int key = k0 + 2 * t4 + (k & 1) + 8 * (k >> 1);
-        on[k] = key < w_end;
+        const int i = 2 * t4 + (k & 1) + 8 * (k >> 1), key = k0 + i;
+        on[k] = key < w_end && !((bad >> (2 * i)) & 3u);
         sv[k] = a.vwin + (ring + (on[k] ? key % R : 0)) * kKvDim + 32 * g;
       }
 #pragma unroll

@@ -704,17 +704,33 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       for (int t = w.e_tb; ok && t < w.tb; ++t, ++gt) {
         const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
         const int k0 = w.it.e_lim + (t - w.it.e_units) * kAtWinUnit, end = w.it.w_lim;
+        // some rows see this tile in part: values that are not finite as in the few-row kernel
+        const bool part = min(k0 + kAtWinUnit, end) > w.it.p + w.it.row0 / a.G + 1;
         ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
         if (!ok) break;
         {
           const int key = k0 + at_key(8 * dw + g);
+          uint32_t bad = 0;
+          if (part) {
+            if (key < end) {
+              const uint4* src = reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 64 * t4);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint4 x = __ldg(src + c);
+                bad |= not_finite_bf162(x.x) | not_finite_bf162(x.y) | not_finite_bf162(x.z) | not_finite_bf162(x.w);
+              }
+            }
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 8);
+            bad |= __shfl_xor_sync(0xffffffffu, bad, 16);
+            if (bad) bad = 0x7fff7fffu;  // NaN, or-ed into the key
+          }
           const uint4* src = reinterpret_cast<const uint4*>(a.kwin + (ring + (key < end ? key % R : 0)) * kKvDim + 64 * t4);
           const uint32_t dst = k_tiles + s * kKvTile + 8192 * t4 + (8 * dw + g) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (key < end) x = __ldg(src + c);
-            sts128(dst + ((c ^ g) << 4), x.x, x.y, x.z, x.w);
+            sts128(dst + ((c ^ g) << 4), x.x | bad, x.y | bad, x.z | bad, x.w | bad);
           }
           fence_proxy_async();
           __syncwarp();
@@ -730,6 +746,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             uint4 y = make_uint4(0u, 0u, 0u, 0u);
             if (key < end) y = __ldg(reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 8 * (4 * dw + t4)));
             x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+            if (part)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[i][k] &= ~((not_finite_bf162(x[i][k]) >> 15) * 0xffffu);
           }
           const uint32_t dst = v_tiles + s * kKvTile + 8 * (4 * dw + t4) * 128;
 #pragma unroll

@@ -255,11 +255,11 @@ int hlwq_kv_scores_window(const uint16_t* q, int64_t m, int64_t ldq, const uint8
  *   reads kv head h).  fp32 softmax and sums, binary16 operands in the rotated
  *   domain, out rounded to bf16 once.  Keys in pages that are not in
  *   [0, num_pages) are left out (HLWQ_DEVERR_KV_RANGE); a row that is left no
- *   key is 0.  A norm that is not finite concerns only the rows that see its
- *   token; a window value that is not may reach earlier queries of its chunk.
- *   A request may have
- *   at most max_new tokens in the step; more raise HLWQ_DEVERR_KV_RANGE and
- *   the rows past the limit may stay unwritten.
+ *   key is 0.  A norm or a window value that is not finite concerns only the
+ *   rows that see its token; such a row may be NaN throughout.  A request may
+ *   have at most max_new tokens in the step; more raise HLWQ_DEVERR_KV_RANGE
+ *   and the rows past the limit may stay unwritten.  out may be Q itself, with
+ *   the same ld.
  *   workspace  device, 16-byte aligned, ws_bytes >= hlwq_workspace_bytes(
  *              HLWQ_OP_KV_ATTENTION, T, max_new, B, q_heads, kv_heads); its
  *              contents need not survive between calls, and calls that may

@@ -396,6 +396,32 @@ def test_attention_tokens_ahead_have_no_say(hl, cb8, new, value):
     _check(out, want, tol, new)
 
 
+@pytest.mark.parametrize("new,R", [(3, 16), (2, 1), (40, 8), (60, 64)])
+@pytest.mark.parametrize("which,value", [(0, float("nan")), (1, float("nan")), (1, float("inf")), (1, float("-inf"))])
+def test_attention_window_tokens_ahead_have_no_say(hl, cb8, new, R, which, value):
+    """One value of the last token's key or value that is not finite, in the window."""
+    args, kw, want, tol = _attend(hl, cb8, [70], [new], 2, 4, 16, R, seed=21)
+    args[6][which][0, 1, (70 + new - 1) % R, 130] = value
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    assert not torch.any(torch.all(torch.isfinite(out[new - 1, 4:]), -1))   # the last token itself, kv head 1
+    out[new - 1, 4:] = torch.from_numpy(want[new - 1, 4:]).to(out.dtype).cuda()
+    _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("past,new,R", [([5000, 40], [1, 1], 128), ([5000], [3], 0), ([3000, 10], [60, 5], 128)])
+def test_attention_into_the_queries(hl, cb8, past, new, R):
+    args, kw, want, tol = _attend(hl, cb8, past, new, 2, 4, 16, R, seed=22)
+    T = sum(new)
+    hl.kv_paged_attention(*args, **kw)
+    rows = args[0].clone()
+    hl.kv_paged_attention(rows, *args[1:], out=rows)
+    torch.cuda.synchronize()
+    _check(kw["out"], want, tol, T)
+    assert torch.equal(rows[:T], kw["out"][:T])
+    assert torch.all(torch.isnan(rows[T:]))
+
+
 @pytest.mark.parametrize("new", [1, 2, 60])
 def test_attention_long_items_are_cut_and_joined(hl, cb8, new):
     """One request, one kv head: every CTA gets a part of the same rows."""
