@@ -20,6 +20,8 @@ namespace {
 constexpr int kKvMaxRequests = 8192;  // prefix sums of all requests in shared memory
 constexpr int kTabThreads = 1024;
 constexpr int kAppThreads = 128;
+constexpr int kAppVector = 512 + 64;  // bytes from vector to vector of a stage: reads of 8 bytes hit all banks
+constexpr int kAppStage = 4 * kAppVector, kAppStages = 3;
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
@@ -27,6 +29,16 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       "mul.rn.f32x2 pd, pa, pb; mov.b64 {%0, %1}, pd; }"
       : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
+}
+
+// cp.async: copies into shared memory that arrive in groups, in order.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Pages of the encoded tokens among n (R slots of window, P tokens to a page).
@@ -222,11 +234,16 @@ __device__ __noinline__ void kv_encode_exact(const uint16_t* src, const double* 
 // and goes through a contiguous range of tokens, so that requests and
 // ring slots are followed from one token to the next instead of being searched for.
 //
-// The vector's lanes read the token that leaves (from the ring or, when the
-// chunk is longer than the window, from the chunk), encode it, and then write
-// the ring slot's new content: slot (p + j) % R of new token j < R ends up with the
-// chunk's last token of that residue, so one group of lanes reads and overwrites
-// a slot and no other touches it.
+// The vector's lanes copy the token that leaves into shared memory (from the ring or,
+// when the chunk is longer than the window, from the chunk; two tokens ahead, by
+// cp.async), encode it, and then write the ring slot's new content: slot (p + j) % R
+// of new token j < R ends up with the chunk's last token of that residue, so one group
+// of lanes reads and overwrites a slot and no other touches it.
+//
+// Rotation: a lane first holds four values of each block of 32 and adds across the
+// blocks, then the vector goes through shared memory once and a lane holds a whole
+// block (whose codes are 12 consecutive bytes); as shuffles the three stages across
+// lanes were 96 instructions instead of 32.
 //
 // Bound: HBM by its bytes (512 read, 98 written per vector); in fact the
 // instructions of the rotation (8 butterfly stages) and of 256 decisions.  The
@@ -234,13 +251,17 @@ __device__ __noinline__ void kv_encode_exact(const uint16_t* src, const double* 
 // nearest binary16.  fp32 decides nearly always.  With u = 2^-24 and n = |x|:
 //   - a butterfly value is off by at most ((1 + u)^8 - 1) sum |x_i| <= 8.01 u 16 n;
 //   - the squares are exact, a path through their sum has 8 additions: n is off by
-//     less than 7 u n, a border mid n (|mid| < 3) by less than 9 u 3 n;
-// so a value farther than 156 u n < 2^-16 n from every border is decided, and a norm
-// farther than 2^-20 n from every binary16 rounding border.  About one vector in
-// a hundred is not, and is encoded by the whole warp in fp64 (kv_encode_exact).
-// 18917 tokens of 4 heads (98 MB): 63 us, 1.6 TB/s, about 1000 instructions per four
-// vectors at 2.5 per cycle; everything in fp64 took 129 us.  More CTAs per SM, or a
-// token ahead in registers, change nothing; the loads alone take 27 us.
+//     less than 6 u n, a border mid n (|mid| < 3) by less than 9 u 3 n;
+// so a value farther than e = 160 u n > 156 u n from every border is decided, and a norm
+// farther than 8 u n = 2^-21 n from every binary16 rounding border (its product with
+// 1 +- 2^-21 is rounded once more).  Distances are tested in pairs: if one of a and b
+// is at most e, and they differ by w, then |a b| <= e (w + e); the pairs 0, t2 and t1, t3
+// have the same slope at both ends, so the test is no wider than single ones.  About one
+// vector in a hundred is not decided, and is encoded by the whole warp in fp64
+// (kv_encode_exact).
+// 18917 tokens of 4 heads (98 MB): 49 us, 2.0 TB/s, 830 warp instructions per four
+// vectors at 2.4 per cycle and SM (five CTAs per SM or 64 threads per CTA: slower); with
+// everything in fp64 129 us; loads and bookkeeping alone 21 us.
 //
 // The decision uses the codebook's symmetry (mid[6 - k] = -mid[k], as Lloyd-Max
 // gives it): three borders for |v|; another codebook goes to fp64 throughout.
@@ -251,6 +272,8 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
                  uint8_t* __restrict__ kp, uint16_t* __restrict__ kn, uint8_t* __restrict__ vp,
                  uint16_t* __restrict__ vn, int64_t num_slots, int P, uint16_t* kwin, uint16_t* vwin, int R) {
   __shared__ double mid[kKvLevels - 1];
+  __shared__ __align__(16) uint8_t swaps[kAppThreads / 32][4 * 4 * kKvDim];      // rotated vectors
+  __shared__ __align__(16) uint8_t stages[kAppThreads / 32][kAppStages * kAppStage];  // vectors under way
   kv_check_codebook(codebook);
   if (threadIdx.x < kKvLevels - 1)
     mid[threadIdx.x] = 0.5 * (static_cast<double>(__ldg(codebook + threadIdx.x)) +
@@ -259,6 +282,9 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
   const bool plain = mid[3] == 0.0 && mid[4] == -mid[2] && mid[5] == -mid[1] && mid[6] == -mid[0] && mid[6] < 3.0;
   const float b1 = static_cast<float>(mid[4]), b2 = static_cast<float>(mid[5]), b3 = static_cast<float>(mid[6]);
   const int lane = threadIdx.x & 31, l8 = lane & 7;
+  uint8_t* swap = swaps[threadIdx.x >> 5] + (lane >> 3) * 4 * kKvDim;
+  const uint8_t* from = stages[threadIdx.x >> 5] + (lane >> 3) * kAppVector + 8 * l8;
+  const uint32_t into = static_cast<uint32_t>(__cvta_generic_to_shared(from)) + 8 * l8;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kAppThreads + threadIdx.x) >> 5;
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kAppThreads / 32);
   const int64_t end = min(T, static_cast<int64_t>(__ldg(cu + B)));
@@ -276,19 +302,22 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
   uint16_t* win = (is_v ? vwin : kwin) + 32 * l8;
   int64_t t = tb + (H == 1 ? lane >> 4 : 0);  // this lane's token
   int b = kv_request_of(cu, B, tb, lane);
+  const uint32_t inv_P = static_cast<uint32_t>((uint64_t(1) << 32) / static_cast<uint32_t>(P));
   int64_t next = -1;                          // the first token behind request b's
   int c0 = 0, p = 0, n = 0, at = 0;           // its first token, lengths, ring slot of token t
+  int last = 0;                               // the last multiple of R below n
   bool live = false;
-  // one token ahead: whether a token leaves as it enters, from where (its values
-  // are requested at once) and to which slot; its own ring slot and what goes there
-  struct {
+  // looked up two tokens ahead: whether a token leaves as it enters, from where (its
+  // copy into a stage begins at once) and to which slot; its own ring slot and
+  // what goes there
+  struct Token {
     bool leaves, ring;
     int64_t slot;
     uint16_t* rs;
     const uint16_t *src, *fresh;
-    uint4 u[4];
-  } a;
-  auto look = [&] {
+  };
+  Token a1, a2;
+  auto look = [&](Token& a, uint32_t stage) {
     a.leaves = false;
     a.ring = false;
     if (!has || t >= te) return;
@@ -303,6 +332,7 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
         next = t + 1;
       }
       n = static_cast<int>(next - c0);
+      last = R ? (n - 1) / R * R : 0;
       at = R ? static_cast<int>((static_cast<uint32_t>(p) + static_cast<uint32_t>(t - c0)) % static_cast<uint32_t>(R)) : 0;
     } else {
       at += toks;
@@ -313,35 +343,44 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
     a.ring = j < R;  // this group owns a ring slot
     a.rs = win + ((static_cast<int64_t>(b) * H + h) * R + at) * kKvDim;
     a.src = a.ring ? a.rs : X + (t - R) * ldx;
-    a.fresh = X + (c0 + static_cast<int64_t>(n - j <= R || !a.ring ? j : j + (n - 1 - j) / R * R)) * ldx;
+    a.fresh = X + (c0 + static_cast<int64_t>(last + j < n ? last + j : last - R + j)) * ldx;  // (of a ring token)
     if (p >= R || j >= R - p) {  // token p + j - R leaves
       a.leaves = true;
       a.slot = __ldg(slot_map + t);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) a.u[c] = reinterpret_cast<const uint4*>(a.src)[c];
+      for (int c = 0; c < 4; ++c) cp_async16(into + stage * kAppStage + 128 * c, a.src - 24 * l8 + 64 * c);
     }
   };
-  look();
+  look(a1, 0);
+  cp_async_commit();
+  t += toks;
+  look(a2, 1);
+  cp_async_commit();
+  uint32_t stage = 0;
   for (int64_t step = tb; step < te; step += toks) {
-    const auto now = a;
+    cp_async_wait<1>();
+    __syncwarp();  // this token's values are there; the stage of the one before is free
+    const Token a = a1;
+    a1 = a2;
+    t += toks;
+    look(a2, stage == 0 ? kAppStages - 1 : stage - 1);  // (its ring slot, if it has one, is another one than this token's)
+    cp_async_commit();
     int64_t slot = -1;
-    if (now.leaves) {
-      slot = now.slot;
+    if (a.leaves) {
+      slot = a.slot;
       if (slot < 0 || slot >= num_slots) {
         raise_device_error(HLWQ_DEVERR_KV_RANGE);
         slot = -1;
       }
     }
-    t += toks;
-    look();  // (its ring slot, if it has one, is another one than this token's)
-    float2 v[16];
+    float2 v[16];  // values 32 c + 4 l8 .. + 3 in v[2 c], v[2 c + 1] (anything without a slot)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint4 u = slot >= 0 ? now.u[c] : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[4 * c + k] = make_float2(bf16x2_lo(wd[k]), bf16x2_hi(wd[k]));
+    for (int c = 0; c < 8; ++c) {
+      const uint2 u = *reinterpret_cast<const uint2*>(from + stage * kAppStage + 64 * c);
+      v[2 * c] = make_float2(bf16x2_lo(u.x), bf16x2_hi(u.x));
+      v[2 * c + 1] = make_float2(bf16x2_lo(u.y), bf16x2_hi(u.y));
     }
+    stage = stage == kAppStages - 1 ? 0 : stage + 1;
     if (__any_sync(0xffffffffu, slot >= 0)) {
       // sum of squares: a tree of 5 + 3 additions
       float2 sq[8];
@@ -352,11 +391,9 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
 #pragma unroll
         for (int k = 0; k < o; ++k) sq[k] = add2(sq[k], sq[k + o]);
       const float ss = oct_sum(sq[0].x + sq[0].y);
-      // rotation: pairs within a register pair, then between pairs, then lanes
-#pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] = make_float2(v[k].x + v[k].y, v[k].x - v[k].y);
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1)
+      // rotation: across the blocks of 32 values, then (a lane taking a block, pieces of
+      // 16 bytes exchanged without bank conflicts) within them
+      auto over = [&](int o) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if ((k & o) == 0) {
@@ -364,46 +401,68 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
             v[k] = add2(x, y);
             v[k + o] = sub2(x, y);
           }
+      };
+      over(2);
+      over(4);
+      over(8);
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        const float sg = (lane & o) ? -1.0f : 1.0f;
-        const float2 s2 = make_float2(sg, sg);
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<float4*>(swap + c * 128 + ((l8 ^ c) << 4)) = make_float4(v[2 * c].x, v[2 * c].y, v[2 * c + 1].x, v[2 * c + 1].y);
+      __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 x = make_float2(__shfl_xor_sync(0xffffffffu, v[k].x, o), __shfl_xor_sync(0xffffffffu, v[k].y, o));
-          v[k] = fma2(v[k], s2, x);  // +-v + x, one rounding
-        }
+      for (int c = 0; c < 8; ++c) {
+        const float4 x = *reinterpret_cast<const float4*>(swap + l8 * 128 + ((l8 ^ c) << 4));
+        v[2 * c] = make_float2(x.x, x.y);
+        v[2 * c + 1] = make_float2(x.z, x.w);
       }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = make_float2(v[k].x + v[k].y, v[k].x - v[k].y);
+      over(1);
+      over(2);
+      over(4);
+      over(8);
       const float nrm = sqrtf(ss);
       const float t1 = b1 * nrm, t2 = b2 * nrm, t3 = b3 * nrm;
-      // |x| between borders m and m + 1: code 3.5 +- (m + 0.5); eight codes are
-      // added up in an fp32 word (24 bits, exact)
+      const float2 m1 = make_float2(t1, t1), m2 = make_float2(t2, t2), m3 = make_float2(t3, t3);
+      // |x| lies between borders m and m + 1 (m = 0 .. 3): code 4 + m, or 3 - m for a
+      // negative x.  A value shifts three sign bits into its word, code bits 2, 1, 0
+      // but for inversions: of x, of |x| - t2 (m < 2), and of the product of
+      // |x|'s distances from t1, t2 and t3 (m even)
       uint32_t q[4];
-      float near = INFINITY;
+      float near1 = INFINITY, near2 = INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float acc = 3.5f * 2396745.0f;  // 3.5 (8^8 - 1) / 7
+        uint32_t acc = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = (e & 1) ? v[4 * c + (e >> 1)].y : v[4 * c + (e >> 1)].x, ax = fabsf(x);
-          const bool p1 = ax > t2;
-          const float tb = p1 ? t3 : t1, d = ax - tb;
-          float mag = p1 ? 2.5f : 0.5f;
-          mag = d > 0.0f ? mag + 1.0f : mag;
-          near = fminf(fminf(near, ax), fminf(fabsf(ax - t2), fabsf(d)));
-          acc = fmaf(copysignf(mag, x), static_cast<float>(1 << (3 * e)), acc);
+        for (int e = 3; e >= 0; --e) {
+          const float2 x = v[4 * c + e], ax = make_float2(fabsf(x.x), fabsf(x.y));
+          const float2 d1 = sub2(ax, m1), d2 = sub2(ax, m2), d3 = sub2(ax, m3);
+          const float2 f = mul2(d1, d3), g = mul2(x, d2), d = mul2(f, d2);
+          near1 = fminf(fminf(near1, fabsf(f.x)), fabsf(f.y));
+          near2 = fminf(fminf(near2, fabsf(g.x)), fabsf(g.y));
+          acc = __funnelshift_l(__float_as_uint(x.y), acc, 1);
+          acc = __funnelshift_l(__float_as_uint(d2.y), acc, 1);
+          acc = __funnelshift_l(__float_as_uint(d.y), acc, 1);
+          acc = __funnelshift_l(__float_as_uint(x.x), acc, 1);
+          acc = __funnelshift_l(__float_as_uint(d2.x), acc, 1);
+          acc = __funnelshift_l(__float_as_uint(d.x), acc, 1);
         }
-        q[c] = static_cast<uint32_t>(acc);
+        const uint32_t neg = acc & 0x924924u;
+        q[c] = (acc ^ (neg >> 1) ^ (neg >> 2)) ^ 0xffffffu;
       }
-      near = fminf(near, __shfl_xor_sync(0xffffffffu, near, 1));
-      near = fminf(near, __shfl_xor_sync(0xffffffffu, near, 2));
-      near = fminf(near, __shfl_xor_sync(0xffffffffu, near, 4));
+      // every |x| is farther than e from 0 and t2, and from t1 and t3
+      const float e = nrm * 0x5p-19f;
+      bool sure = near2 > e * (t2 + e) && near1 > e * (t3 - t1 + e);
+      sure = (__ballot_sync(0xffffffffu, sure) >> (lane & 24) & 0xffu) == 0xffu;
       // the norm's rounding to binary16: both ends of its interval agree
-      const uint32_t h0 = __half_as_ushort(__float2half_rn(nrm * (1.0f - 0x1p-20f)));
-      const uint32_t h1 = __half_as_ushort(__float2half_rn(nrm * (1.0f + 0x1p-20f)));
-      const bool sure = plain && ss > 0x1p-100f && ss < 0x1p100f && near > nrm * 0x1p-16f && h0 == h1;
-      const int64_t page = slot >> 31 ? slot / P : static_cast<int64_t>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(P));
-      const int64_t row = page * H * P + static_cast<int64_t>(h) * P + (slot - page * P);
+      const uint32_t h0 = __half_as_ushort(__float2half_rn(nrm * (1.0f - 0x1p-21f)));
+      const uint32_t h1 = __half_as_ushort(__float2half_rn(nrm * (1.0f + 0x1p-21f)));
+      sure = sure && plain && ss > 0x1p-100f && ss < 0x1p100f && h0 == h1;
+      // page and place in it: below 2^32 by the reciprocal, which is at most 1 short
+      uint32_t page = __umulhi(static_cast<uint32_t>(slot), inv_P), place = static_cast<uint32_t>(slot) - page * P;
+      if (place >= static_cast<uint32_t>(P)) ++page, place -= P;
+      if (slot >> 32 > 0) page = static_cast<uint32_t>(slot / P), place = static_cast<uint32_t>(slot % P);
+      const int64_t row = static_cast<int64_t>(page) * (H * P) + (h * P + place);
       uint8_t* out = (is_v ? vp : kp) + row * kKvBytes;
       uint16_t* out_n = (is_v ? vn : kn) + row;
       if (slot >= 0 && sure) {
@@ -415,19 +474,19 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
       }
       uint32_t again = __ballot_sync(0xffffffffu, slot >= 0 && !sure && l8 == 0);
       while (again) {
-        const int from = __ffs(static_cast<int>(again)) - 1;
+        const int src_lane = __ffs(static_cast<int>(again)) - 1;
         again &= again - 1;
-        kv_encode_exact(reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(now.src), from)),
+        kv_encode_exact(reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(a.src), src_lane)),
                         mid,
-                        reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), from)),
-                        reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_n), from)),
+                        reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), src_lane)),
+                        reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_n), src_lane)),
                         lane);
       }
       __syncwarp();  // the ring has been read by every lane
     }
-    if (now.ring) {
+    if (a.ring) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(now.rs)[c] = __ldg(reinterpret_cast<const uint4*>(now.fresh) + c);
+      for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(a.rs)[c] = __ldg(reinterpret_cast<const uint4*>(a.fresh) + c);
     }
   }
 }
