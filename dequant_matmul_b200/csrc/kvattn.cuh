@@ -736,8 +736,8 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
     // ---- window keys, 16 at a time and as they are: bf16 operands, scores exact to
     // fp32, p in two bf16 parts (16 bits).  In a tile that some rows see in part, a value
-    // that is not finite is carried by its key's score: the rows that see it come out
-    // NaN, and 0 * inf does not reach those that do not.
+    // that is not finite is carried by the sums of the rows that see it (they come out
+    // NaN), and 0 * inf does not reach those that do not.
     const int w_first = it.e_lim + (max(ta, it.e_units) - it.e_units) * kRowWinUnit;
     const int w_end = min(it.e_lim + (tb - it.e_units) * kRowWinUnit, it.w_lim);
     if (w_first < w_end) {
@@ -748,19 +748,6 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {
       const int R = static_cast<int>(a.R);
       const int64_t ring = (static_cast<int64_t>(it.b) * a.H + h) * R;
-      uint32_t bad = 0;  // bits 2 i, 2 i + 1: halves of key i's value
-      if (min(k0 + 16, w_end) > it.p + it.row0 / a.G + 1) {
-        const int key = k0 + (lane >> 1);
-        if (key < w_end) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.vwin + (ring + key % R) * kKvDim + 128 * (lane & 1));
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 x = __ldg(src + c);
-            bad |= not_finite_bf162(x.x) | not_finite_bf162(x.y) | not_finite_bf162(x.z) | not_finite_bf162(x.w);
-          }
-        }
-        bad = __ballot_sync(0xffffffffu, bad != 0u);
-      }
       float d[1][NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) d[0][nt][0] = d[0][nt][1] = d[0][nt][2] = d[0][nt][3] = 0.0f;
@@ -782,13 +769,6 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
         }
       }
-      if (bad) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((bad >> (2 * g + 16 * (k >> 1))) & 3u) d[0][nt][k] = NAN;
-      }
       const float one[1][2] = {{1.0f, 1.0f}};
       const int key[1] = {k0 + g}, end[1] = {w_end};
       score(d, one, key, end);
@@ -803,10 +783,12 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         }
       const uint16_t* sv[4];
       bool on[4];
+      const bool part = min(k0 + 16, w_end) > it.p + it.row0 / a.G + 1;
+      uint32_t bad = 0;  // bit i: key k0 + i
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int i = 2 * t4 + (k & 1) + 8 * (k >> 1), key = k0 + i;
-        on[k] = key < w_end && !((bad >> (2 * i)) & 3u);
+        const int key = k0 + 2 * t4 + (k & 1) + 8 * (k >> 1);
+        on[k] = key < w_end;
         sv[k] = a.vwin + (ring + (on[k] ? key % R : 0)) * kKvDim + 32 * g;
       }
 #pragma unroll
@@ -818,6 +800,15 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           if (on[k]) u = __ldg(reinterpret_cast<const uint4*>(sv[k]) + c);
           x[k][0] = u.x, x[k][1] = u.y, x[k][2] = u.z, x[k][3] = u.w;
         }
+        if (part) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (not_finite_bf162(x[k][0]) | not_finite_bf162(x[k][1]) | not_finite_bf162(x[k][2]) | not_finite_bf162(x[k][3])) {
+              bad |= 1u << (2 * t4 + (k & 1) + 8 * (k >> 1));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[k][i] &= ~((not_finite_bf162(x[k][i]) >> 15) * 0xffffu);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410), a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
@@ -828,6 +819,14 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             mma_16816_bf16(o[nt][4 * c + i], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
           }
         }
+      }
+      if (part) {
+        bad = __reduce_or_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (bad & ((1u << max(0, min(16, lim[nt][k] - k0))) - 1u)) l[nt][k] = NAN;
       }
     }
 

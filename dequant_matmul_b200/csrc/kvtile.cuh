@@ -704,7 +704,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       for (int t = w.e_tb; ok && t < w.tb; ++t, ++gt) {
         const uint32_t s = gt & 1u, par = (gt >> 1) & 1u;
         const int k0 = w.it.e_lim + (t - w.it.e_units) * kAtWinUnit, end = w.it.w_lim;
-        // some rows see this tile in part: values that are not finite as in the few-row kernel
+        // some rows see this tile in part: a value that is not finite is carried by its
+        // key, as an encoded one's norm is
         const bool part = min(k0 + kAtWinUnit, end) > w.it.p + w.it.row0 / a.G + 1;
         ok = at_wait_warp(k_empty + 8 * s, par ^ 1u);
         if (!ok) break;
