@@ -363,7 +363,8 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kStage = 3136;  // 16 keys: K codes 1536, V codes 1536, K norms 32, V norms 32
+constexpr int kStageNorms = 2 * 16 * kKvBytes;  // 16 keys: K codes, V codes,
+constexpr int kStage = kStageNorms + 64;        // K norms, V norms
 constexpr int kStages = 4;
 // An item's beginning and end (rotations, joining the warps) take about 6 us where a
 // unit takes 1.3; a window tile of 16 about as long as a unit.
@@ -594,7 +595,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
               cp_async16(dst + 16 * lane + 512 * c, ks + 512 * c);
               cp_async16(dst + 1536 + 16 * lane + 512 * c, vs + 512 * c);
             }
-            if (lane < 16) cp_async4(dst + 3072 + 4 * lane, (lane < 8 ? a.kn : a.vn) + row + 2 * (lane & 7));
+            if (lane < 16) cp_async4(dst + kStageNorms + 4 * lane, (lane < 8 ? a.kn : a.vn) + row + 2 * (lane & 7));
           }
           row += 16;
         }
@@ -626,7 +627,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
                 const uint2 y = lds64(src + 8 * c);
                 x[i][k][2 * c] = y.x, x[i][k][2 * c + 1] = y.y;
               }
-              const uint32_t n = st + i * kStage + 3072 + 2 * (key_g + 8 * k);
+              const uint32_t n = st + i * kStage + kStageNorms + 2 * (key_g + 8 * k);
               nk[i][k] = lds_half(n);
               nv[i][k] = lds_half(n + 32);
             }
