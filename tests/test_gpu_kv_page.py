@@ -181,6 +181,35 @@ def test_append_near_the_borders(hl, cb8):
         assert np.array_equal(nr.transpose(1, 2).reshape(n).cpu().numpy(), want["norms"].view(np.uint16))
 
 
+@pytest.mark.parametrize("levels", [[-2.1, -1.2, -0.7, -0.2, 0.3, 0.7, 1.3, 2.2], [-1.0, -0.6, -0.3, -0.1, 0.1, 0.3, 0.6, 1.0],
+                                    [-4.5, -2.5, -1.5, -0.5, 0.5, 1.5, 2.5, 4.5]])
+def test_append_with_another_codebook(hl, levels):
+    """Not symmetric, narrower, with borders beyond 3; and chunks of several requests."""
+    H, P, T = 3, 16, 700
+    X = _rows(T, H, 31)
+    cb = np.array(levels, np.float32)
+    x = X.double().reshape(-1, 256).numpy()
+    had = np.array([[1.0]])
+    while had.shape[0] < 256:
+        had = np.block([[had, had], [had, -had]])
+    norm = np.sqrt((x * x).sum(-1))
+    y = x @ had / np.where(norm > 0, norm, 1.0)[:, None]
+    mid = (cb[1:].astype(np.float64) + cb[:-1].astype(np.float64)) / 2
+    want = (y[:, :, None] > mid).sum(-1)
+    tell = np.min(np.abs(y[:, :, None] - mid), axis=-1) > 1e-12   # two fp64 evaluations agree here
+    n = -(-T // P)
+    pages = [(torch.zeros(n, H, P, 96, dtype=torch.uint8, device="cuda"),
+              torch.zeros(n, H, P, dtype=torch.uint16, device="cuda")) for _ in range(2)]
+    hl.kv_paged_append(X.cuda(), X.cuda(), torch.arange(T, device="cuda"), _ints([0, 1, 1, 300, T]), _ints([0, 0, 5, 9]), *pages,
+                       None, torch.from_numpy(cb).cuda())
+    torch.cuda.synchronize()
+    for p, nr in pages:
+        got = p.transpose(1, 2).reshape(n * P * H, 96)[:T * H].cpu().numpy()
+        assert np.array_equal(O.unpack_codes(got, bits=3)[tell], want[tell])
+        assert np.array_equal(nr.transpose(1, 2).reshape(-1)[:T * H].cpu().numpy(), norm.astype(np.float16).view(np.uint16))
+    assert hl.device_error() == 0
+
+
 def test_append_with_slots_out_of_range(hl, cb8):
     """A slot that is not one of the pool is not written, and is reported."""
     hl.device_error()
