@@ -309,10 +309,18 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ float lds_half(uint32_t a) {
+__device__ __forceinline__ uint16_t lds16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
-  return half_bits_to_float(v);
+  return v;
+}
+
+__device__ __forceinline__ float lds_half(uint32_t a) { return half_bits_to_float(lds16(a)); }
+
+// The least power of two above a binary16 norm, as an exponent: -14 (below 2^-14)
+// to 16; 17 when it is not finite.
+__device__ __forceinline__ float log2_above(uint16_t h) {
+  return __uint_as_float(0x43000000u | ((h & 0x7c00u) << 6)) - 142.0f;  // 128 + exponent field, less its bias
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -342,15 +350,16 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // instructions for two values.
 //
 // P^T comes out of S^T's registers by two 8 x 8 transposes; row sums
-// stay in the lane until the end.  The running reference of a row's maximum is
-// raised only when a score exceeds it by 8 (in powers of two; p stays below 2^8): the
-// sums are the same, most steps need no exchange between lanes.  A value's norm
-// rides on p; p n is kept in binary16's range by a power of two that follows the
-// largest norm (fv), so it does not overflow and what is lost is below 2^-29 of the
-// largest term.  O^T's registers hold 32 consecutive dims of two rows: the
-// rotation back is five in-register and three shuffle stages.  The window's keys
-// come after it and are multiplied as they are, un-rotated bf16 with the query's
-// own bits.
+// stay in the lane until the end.  A value's norm rides on p, and a row's running
+// reference m follows its largest score + log2 norm, the size of the term p n: it is
+// raised only when one exceeds it by 8 (in powers of two), so most steps need no exchange
+// between lanes.  Then p n < 2^8 (p itself, at most 2^22, is summed in fp32), and kNvScale
+// brings it to where binary16 has 11 bits for it down to 2^-20 of the row's largest
+// term and to 2^-31 of that term below, whatever the norms of keys are that the row
+// does not see or gives no weight.  O^T's registers hold 32 consecutive dims of two
+// rows: the rotation back is five in-register and three shuffle stages.  The window's
+// keys come after it and are multiplied as they are, un-rotated bf16 with the
+// query's own bits.
 //
 // Bound: HBM by its bytes (196 per token and kv head); in fact integer instructions
 // and shared-memory reads, one warp instruction in five a table read.  64 requests
@@ -373,6 +382,7 @@ constexpr int kRowWinUnit = 16;
 constexpr int kTabBytes = 64 * 128;
 constexpr float kMinM = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNvScale = 128.0f;  // on the norms of values: p n kNvScale < 2^15
 
 template <int NT>
 struct RowCfg {
@@ -491,7 +501,6 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
     float o[NT][16][4], m[NT][2], l[NT][2], qm[NT][2];
     int lim[NT][2];
-    float fv = 2147483648.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -506,39 +515,50 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       }
 
     // scores of M tiles of 16 keys, times their factors f[.][0] (this lane's first
-    // key, index key[.]) and f[.][1] (8 further); keys from end[.] on are not there.
-    // The rows' references follow; d becomes p = exp2(s - reference), up to 2^8
-    auto score = [&](auto& d, const auto& f, const auto& key, const auto& end) {
+    // key, index key[.]) and f[.][1] (8 further), with the log2 of their values' size
+    // in size[.][.]; keys from end[.] on are not there.  The rows' references follow;
+    // d becomes p = exp2(s - reference).  Rounded so that p size never passes 2^8
+    auto score = [&](auto& d, const auto& f, const auto& size, const auto& key, const auto& end) {
       constexpr int M = sizeof(key) / sizeof(key[0]);
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+          const bool none = m[nt][k] == kMinM;  // no key so far
+          const float ref = none ? 0.0f : m[nt][k];
           float x = -INFINITY;
 #pragma unroll
           for (int i = 0; i < M; ++i) {
             const int see = min(lim[nt][k], end[i]);
-            d[i][nt][k] = key[i] < see ? d[i][nt][k] * (f[i][0] * qm[nt][k]) : -INFINITY;
-            d[i][nt][2 + k] = key[i] + 8 < see ? d[i][nt][2 + k] * (f[i][1] * qm[nt][k]) : -INFINITY;
-            x = fmaxf(x, fmaxf(d[i][nt][k], d[i][nt][2 + k]));
+            d[i][nt][k] = key[i] < see ? fmaf(d[i][nt][k], f[i][0] * qm[nt][k], -ref) : -INFINITY;
+            d[i][nt][2 + k] = key[i] + 8 < see ? fmaf(d[i][nt][2 + k], f[i][1] * qm[nt][k], -ref) : -INFINITY;
+            x = fmaxf(x, fmaxf(d[i][nt][k] + size[i][0], d[i][nt][2 + k] + size[i][1]));
           }
-          over |= x > m[nt][k] + 8.0f;
+          over |= x > (none ? kMinM : 8.0f);
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float x = m[nt][k];
+            const float ref = m[nt][k] == kMinM ? 0.0f : m[nt][k];
+            float x = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < M; ++i) x = fmaxf(x, fmaxf(d[i][nt][k], d[i][nt][2 + k]));
+            for (int i = 0; i < M; ++i)
+              x = fmaxf(x, fmaxf(__fadd_ru(d[i][nt][k], size[i][0]), __fadd_ru(d[i][nt][2 + k], size[i][1])));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float c = ex2(m[nt][k] - x);
-            m[nt][k] = x;
+            const float nm = fmaxf(m[nt][k], __fadd_ru(ref, x)), c = ex2(m[nt][k] - nm);
+            const float step = nm == kMinM ? 0.0f : __fadd_rd(ref, -nm);
+            m[nt][k] = nm;
             l[nt][k] *= c;
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+              d[i][nt][k] += step;
+              d[i][nt][2 + k] += step;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               o[nt][i][k] *= c;
@@ -551,7 +571,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
         for (int i = 0; i < M; ++i) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) d[i][nt][k] = ex2(d[i][nt][k] - m[nt][k & 1]);
+          for (int k = 0; k < 4; ++k) d[i][nt][k] = ex2(d[i][nt][k]);
           l[nt][0] += d[i][nt][0] + d[i][nt][2];
           l[nt][1] += d[i][nt][1] + d[i][nt][3];
         }
@@ -612,7 +632,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         cp_async_wait<1>();
         __syncwarp();
         const uint32_t st = wbuf + stage * 2 * kStage;
-        float d[2][NT][4], nk[2][2], nv[2][2];
+        float d[2][NT][4], nk[2][2], nv[2][2], size[2][2];
         const int key[2] = {k0 + key_g, k0 + 16 + key_g};
         const int end[2] = {there & 1u ? k_end : 0, there & 2u ? k_end : 0};
         {
@@ -627,9 +647,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
                 const uint2 y = lds64(src + 8 * c);
                 x[i][k][2 * c] = y.x, x[i][k][2 * c + 1] = y.y;
               }
-              const uint32_t n = st + i * kStage + kStageNorms + 2 * (key_g + 8 * k);
-              nk[i][k] = lds_half(n);
-              nv[i][k] = lds_half(n + 32);
+              nk[i][k] = lds_half(st + i * kStage + kStageNorms + 2 * (key_g + 8 * k));
             }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -660,40 +678,28 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             }
           }
         }
-        score(d, nk, key, end);
-        bool high = false;
-        float top = 0.0f;
+        uint16_t hv[2][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float x = key[i] + 8 * k < end[i] ? nv[i][k] : 0.0f;
-            high |= x * fv > 128.0f;
-            top = fmaxf(top, x);
+            hv[i][k] = lds16(st + i * kStage + kStageNorms + 32 + 2 * (key_g + 8 * k));
+            size[i][k] = log2_above(hv[i][k]);
           }
-        if (__any_sync(0xffffffffu, high)) {
+        score(d, nk, size, key, end);
 #pragma unroll
-          for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-          const int e = min(144, static_cast<int>(__float_as_uint(top) >> 23) + 1);  // top < 2^(e - 127)
-          const float nf = __uint_as_float(static_cast<uint32_t>(259 - e) << 23), f = nf / fv;  // top nf in [16, 32)
-          fv = nf;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[nt][i][k] *= f;
-        }
+          for (int k = 0; k < 2; ++k) nv[i][k] = half_bits_to_float(hv[i][k]) * kNvScale;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t b[NT][2];
-          const float f0 = nv[i][0] * fv, f1 = nv[i][1] * fv;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             // a key that is masked out has no say, whatever its norm is (NaN stays NaN)
             float p[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = d[i][nt][k] == 0.0f ? 0.0f : d[i][nt][k] * (k < 2 ? f0 : f1);
+            for (int k = 0; k < 4; ++k) p[k] = d[i][nt][k] == 0.0f ? 0.0f : d[i][nt][k] * nv[i][k >> 1];
             b[nt][0] = transpose_8x8(pack_half2(p[0], p[1]));
             b[nt][1] = transpose_8x8(pack_half2(p[2], p[3]));
           }
@@ -712,9 +718,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       __syncwarp();
     }
 
-    // ---- out of the rotated domain: O^T <- H O^T / (256 fv), in registers
+    // ---- out of the rotated domain: O^T <- H O^T / (256 kNvScale), in registers
     if (ta < e_tb) {
-      const float f = 1.0f / (256.0f * fv);
+      constexpr float f = 1.0f / (256.0f * kNvScale);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -770,9 +776,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
         }
       }
-      const float one[1][2] = {{1.0f, 1.0f}};
+      const float one[1][2] = {{1.0f, 1.0f}}, zero[1][2] = {{0.0f, 0.0f}};
       const int key[1] = {k0 + g}, end[1] = {w_end};
-      score(d, one, key, end);
+      score(d, one, zero, key, end);
       uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)

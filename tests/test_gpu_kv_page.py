@@ -647,3 +647,78 @@ def test_long_cache_offsets(hl, cb8):
     torch.cuda.synchronize()
     _check(out, want, tol, T)
     _check(one, want[-1:], tol[-1:], 1)
+
+
+# ------------------------------------------------------------------ values of very different size in one row
+def _attend_on(hl, cb8, X, Y, Q, n, R, G, P=16):
+    """Call, reference and tolerance of the last n queries Q over one request's keys X
+    and values Y [N][H][256], all from the oracle's state."""
+    N, H, _ = X.shape
+    pages = -(-N // P)
+    table, cu, slots, _ = O.kv_block_tables([0], [N], list(range(pages)), np.full((1, pages), -1), P, R, N)
+    st = [O.kv_paged_append(x, slots, cu, [0], np.zeros((pages, H, P, 96), np.uint8), np.zeros((pages, H, P), np.float16),
+                            np.zeros((1, H, R, 256)), R) for x in (X, Y)]
+    want, tol = O.kv_paged_attention(Q, [0, n], [N - n], table, *st, R, 0.0625)
+    dev = [(_dev_pages(p, nr), torch.from_numpy(w).to(torch.bfloat16).cuda() if R else None) for p, nr, w in st]
+    out = torch.full(Q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    args = (Q.cuda(), _ints([0, n]), _ints([N - n]), _ints(table), dev[0][0], dev[1][0],
+            (dev[0][1], dev[1][1]) if R else None, cb8, n)
+    return args, dict(out=out), want, tol
+
+
+def _small_values(N, n, Hq, seed):
+    """Keys, values of norm 2^-12 and queries near a common direction, which is returned."""
+    base = _rows(1, 1, seed, False)[0, 0]
+    Q = (base + 0.2 * _rows(n, Hq, seed + 1, False).float()).to(torch.bfloat16)
+    return _rows(N, 1, seed + 2, False), (_rows(N, 1, seed + 3, False).float() * 2.0 ** -16).to(torch.bfloat16), Q, base.float()
+
+
+FEW = [(1, 6), (3, 4)]
+
+
+@pytest.mark.parametrize("new,G", FEW)
+def test_attention_large_value_without_weight(hl, cb8, new, G):
+    """A value of norm 60000 whose key is far from every query (weight e^-48), among
+    values of norm 2^-12: these are the row's terms and keep their accuracy."""
+    N = 150 + new
+    for heavy in (3, 40, 149):
+        X, Y, Q, base = _small_values(N, new, G, 50)
+        X[heavy, 0] = (-3 * base).to(torch.bfloat16)
+        Y[heavy, 0] = 3750.0 * torch.sign(Y[heavy, 0].float()).to(torch.bfloat16)
+        args, kw, want, tol = _attend_on(hl, cb8, X, Y, Q, new, 0, G)
+        out = hl.kv_paged_attention(*args, **kw)
+        torch.cuda.synchronize()
+        assert np.all(np.linalg.norm(want, axis=-1) < 2.0 ** -12)
+        _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("new,G", [c for c in FEW if c[0] > 1])
+@pytest.mark.parametrize("value", [60000.0, float("inf")])
+def test_attention_large_value_ahead(hl, cb8, new, G, value):
+    """The last token's value is large or infinite: rows that do not see it keep the
+    accuracy that their own values of norm 2^-12 have."""
+    N = 60 + new
+    X, Y, Q, _ = _small_values(N, new, G, 60)
+    args, kw, want, tol = _attend_on(hl, cb8, X, Y, Q, new, 0, G)
+    args[5][1].view(torch.float16)[int(args[3][0, (N - 1) // 16]), 0, (N - 1) % 16] = value
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    _check(out[:new - 1], want[:new - 1], tol[:new - 1], new - 1)
+
+
+@pytest.mark.parametrize("new,G", FEW)
+def test_attention_value_norms_that_grow(hl, cb8, new, G):
+    """The largest term comes late, by its score, by its norm, or by both: what came
+    before is rescaled, and zero norms and the smallest ones do not disturb it."""
+    N = 300 + new
+    for grow_key, grow_value in ((0.0, 2.0), (3.0, 0.0), (3.0, -2.0), (-1.0, 2.0)):
+        X, Y, Q, base = _small_values(N, new, G, 70)
+        Y = Y.float() * 2.0 ** 6
+        at = torch.arange(N)[:, None, None] / N
+        X = (X.float() + grow_key * at * base).to(torch.bfloat16)
+        Y = (Y * torch.exp2(6 * grow_value * at)).to(torch.bfloat16)
+        Y[7], Y[8] = 0, 2.0 ** -28   # a zero vector, a norm of 2^-24
+        args, kw, want, tol = _attend_on(hl, cb8, X, Y, Q, new, 0, G)
+        out = hl.kv_paged_attention(*args, **kw)
+        torch.cuda.synchronize()
+        _check(out, want, tol, new)
