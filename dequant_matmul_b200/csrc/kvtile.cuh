@@ -64,7 +64,8 @@ constexpr int kCodeStages = 3;
 constexpr int kNormOff = 2 * 4 * kGrp;               // 12416
 constexpr int kMaskOff = kNormOff + 256;
 constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
-constexpr int kNrmSlot = 128 * 4 + 16;               // K norms, V norms, maxima of V's, mask
+constexpr int kNrmSlot = 192 * 4 + 16;               // K norms, V norms (kNvScale times), log2_above of V's, mask
+constexpr int kSlotMask = 192 * 4;
 constexpr float kMinQm = 1e-36f;                     // a zero scale: masked keys (-inf) stay masked, the others equal
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 constexpr int kAtSmem = 8192 /*align*/ + 8192 /*table*/ + 4 * kKvTile + kCodeStages * kCodeStage + 4 * kNrmSlot + 512 +
@@ -170,6 +171,14 @@ __device__ __forceinline__ void tc_ld4(uint32_t taddr, uint32_t (&v)[4]) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "r"(taddr)
                : "memory");
+}
+
+__device__ __forceinline__ float2 fma2_up(float2 a, float2 b, float2 c) {  // rounded upwards
+  float2 r;
+  asm("{ .reg .b64 pa, pb, pc, pd; mov.b64 pa, {%2, %3}; mov.b64 pb, {%4, %5}; mov.b64 pc, {%6, %7};\n\t"
+      "fma.rp.f32x2 pd, pa, pb, pc; mov.b64 {%0, %1}, pd; }"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
 }
 
 // 64 columns of this warp's rows <-> registers.
@@ -347,9 +356,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         KvCut cut;
         if (w.note(share, cut)) cuts[blockIdx.x] = cut;
       }
-      // m: the row's reference; lf: log2 of the power of two that keeps p n in
-      // binary16's range, in l as in O; l: this thread's share of the row's sum
-      float m = kMinM, l = 0.0f, lf = 31.0f, qm = 0.0f;
+      // m: the row's reference, which follows its largest p n as in the few-row
+      // kernel; l: this thread's share of the row's sum
+      float m = kMinM, l = 0.0f, qm = 0.0f, inv_qm = 0.0f;
       bool started = false;  // O holds something
 
       // One tile: S(gt) -> P(gt).  win: window keys, p in two bf16 parts.  This
@@ -380,7 +389,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
           }
         }
-        const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + 520);  // 16-key groups whose page is there
+        const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + kSlotMask);  // 16-key groups whose page is there
         const int see = min(lim, end) - k0;
         if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
           const int sh = see - 2 * half;
@@ -393,35 +402,29 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             if (f + 48 >= sh || !(there & 8u)) v[i][1].y = -INFINITY;
           }
         }
-        float mx = fmaxf(fmaxf(v[0][0].x, v[0][0].y), fmaxf(v[0][1].x, v[0][1].y)), my = mx;
+        // the largest score + log2 norm, rounded so that p n never passes 2^8
+        float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
-          mx = fmaxf(fmaxf(v[i][0].x, v[i][0].y), mx);
-          my = fmaxf(fmaxf(v[i][1].x, v[i][1].y), my);
+        for (int i = 0; i < 8; ++i) {
+          float2 x = v[i][0], y = v[i][1];
+          if constexpr (!kWin) {
+            const float4 z = lds_f4(nb + 512 + 32 * i);
+            x = fma2_up(make_float2(z.x, z.y), make_float2(inv_qm, inv_qm), x);
+            y = fma2_up(make_float2(z.z, z.w), make_float2(inv_qm, inv_qm), y);
+          }
+          mx = fmaxf(fmaxf(x.x, x.y), mx);
+          my = fmaxf(fmaxf(y.x, y.y), my);
         }
-        mx = fmaxf(mx, my) * qm;
-        float corr = 1.0f;
+        mx = __fmul_ru(fmaxf(mx, my), qm);
         // also: both halves of S have been read, P may take its place
-        bool fix = pair_any(quarter, !got || mx > m + 8.0f);
-        if (fix) {  // seldom
+        if (pair_any(quarter, !got || mx > __fadd_rd(m, 8.0f))) {  // seldom
           if (pair_any(quarter, !got)) return false;
           *mine = mx;
           pair_sync(quarter);
           const float nm = fmaxf(m, fmaxf(mx, *other));
-          corr = ex2(m - nm);
+          const float corr = ex2(m - nm);
           m = nm;
           pair_sync(quarter);
-        }
-        if constexpr (!kWin) {
-          const float vm = __uint_as_float(max(lds32(nb - 16 * half + 512), lds32(nb - 16 * half + 516)));
-          if (vm * ex2(lf) > 128.0f) {  // the same for all threads
-            const int e = min(144, static_cast<int>(__float_as_uint(vm) >> 23) + 1);  // vm < 2^(e - 127)
-            corr *= ex2(static_cast<float>(132 - e) - lf);                            // vm 2^(132 - e) in [16, 32)
-            lf = static_cast<float>(132 - e);
-            fix = true;
-          }
-        }
-        if (fix) {
           l *= corr;
           if (started) {  // rescale O once the product before has been added
             if (pair_any(quarter, !pv_done(gt - 1))) return false;
@@ -436,8 +439,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             }
           }
         }
-        // p 2^lf = 2^(s qm - m + lf), and its sum
-        const float2 q2 = make_float2(qm, qm), b2 = make_float2(lf - m, lf - m);
+        // p = 2^(s qm - m), and its sum
+        const float2 q2 = make_float2(qm, qm), b2 = make_float2(-m, -m);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -517,6 +520,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         // |q H| <= 16 |q|: with |q| brought into [16, 32) no coordinate passes 512
         const float sc = sgn * pow2_scale(sqrtf(half ? *other + ss : ss + *other), inv);
         qm = fmaxf(fabsf(a.scale) * inv * (kLog2e / 256.0f), kMinQm);
+        inv_qm = 1.0f / qm;
         across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -534,10 +538,10 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           ok = false;
           break;
         }
-        // O out of the rotated domain, and the sums with the same factor
+        // O out of the rotated domain
         within_blocks(row, half);
         pair_sync(quarter);
-        const float f = ex2(-8.0f - lf);
+        constexpr float f = 1.0f / (256.0f * kNvScale);
         across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -547,10 +551,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             tc_st16(row + kColO + 64 * k + c, x);
           }
         });
-        l *= ex2(-lf);
         pair_sync(quarter);
       }
-      lf = 0.0f;
       if (w.e_tb < w.tb) {
         // window units: Q as it is
 #pragma unroll 1
@@ -625,16 +627,16 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         const int left = w.it.e_lim - t * kUnit;  // keys from here to the end
         if (tid < 128) {
           const int n = tid & 63, key = at_key(n);
-          const float nk = lds_half(st + kNormOff + 2 * key), nv = lds_half(st + kNormOff + 128 + 2 * key);
+          const uint16_t hv = lds16(st + kNormOff + 128 + 2 * key);
+          const float nk = lds_half(st + kNormOff + 2 * key), nv = half_bits_to_float(hv);
           // A value's norm that is not finite goes into its key's: the rows that see it
           // come out NaN, and 0 * inf does not reach those that do not.
-          float x = tid < 64 ? (isfinite(nv) ? nk : NAN) : (isfinite(nv) ? nv : 0.0f);
+          float x = tid < 64 ? (isfinite(nv) ? nk : NAN) : (isfinite(nv) ? nv * kNvScale : 0.0f);
           if (key >= left || !((there >> (key >> 4)) & 1u)) x = 0.0f;
           const uint32_t slot = nrm + (gt & 3u) * kNrmSlot;
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + 4 * tid), "f"(x) : "memory");
-          const uint32_t mx = __reduce_max_sync(0xffffffffu, x == x ? __float_as_uint(x) : 0u);
-          if (tid >= 64 && lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 512 + 4 * ((tid - 64) >> 5)), "r"(mx) : "memory");
-          if (tid == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + 520), "r"(there) : "memory");
+          if (tid >= 64) asm volatile("st.shared.f32 [%0], %1;" ::"r"(slot + 256 + 4 * tid), "f"(log2_above(hv)) : "memory");
+          if (tid == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + kSlotMask), "r"(there) : "memory");
         }
         {  // K: key of row 8 dw + g, dims 64 t4 .. + 63
           const uint32_t src = st + (g & 3) * kGrp + (2 * (g >> 2) + (dw & 1) + 4 * (dw >> 1)) * kKvBytes + 24 * t4;

@@ -673,10 +673,10 @@ def _small_values(N, n, Hq, seed):
     return _rows(N, 1, seed + 2, False), (_rows(N, 1, seed + 3, False).float() * 2.0 ** -16).to(torch.bfloat16), Q, base.float()
 
 
-FEW = [(1, 6), (3, 4)]
+ROWS = [(1, 6), (3, 4), (20, 6), (40, 4)]   # few rows per kv head, and tiles of 128
 
 
-@pytest.mark.parametrize("new,G", FEW)
+@pytest.mark.parametrize("new,G", ROWS)
 def test_attention_large_value_without_weight(hl, cb8, new, G):
     """A value of norm 60000 whose key is far from every query (weight e^-48), among
     values of norm 2^-12: these are the row's terms and keep their accuracy."""
@@ -692,7 +692,7 @@ def test_attention_large_value_without_weight(hl, cb8, new, G):
         _check(out, want, tol, new)
 
 
-@pytest.mark.parametrize("new,G", [c for c in FEW if c[0] > 1])
+@pytest.mark.parametrize("new,G", [c for c in ROWS if c[0] > 1])
 @pytest.mark.parametrize("value", [60000.0, float("inf")])
 def test_attention_large_value_ahead(hl, cb8, new, G, value):
     """The last token's value is large or infinite: rows that do not see it keep the
@@ -706,7 +706,7 @@ def test_attention_large_value_ahead(hl, cb8, new, G, value):
     _check(out[:new - 1], want[:new - 1], tol[:new - 1], new - 1)
 
 
-@pytest.mark.parametrize("new,G", FEW)
+@pytest.mark.parametrize("new,G", ROWS)
 def test_attention_value_norms_that_grow(hl, cb8, new, G):
     """The largest term comes late, by its score, by its norm, or by both: what came
     before is rescaled, and zero norms and the smallest ones do not disturb it."""
