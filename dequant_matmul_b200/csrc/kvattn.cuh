@@ -239,16 +239,92 @@ __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The centroids as binary16: c times a scale of kCentroidScales between two powers of two
+// (the largest |c| goes to [2^7, 2^9)), the one under which the 8 roundings agree best
+// with one common factor.  That factor goes back into the scores and the outputs
+// in fp32.  The roundings come the same way at every use of a code and do not
+// average out: under a power of two the Lloyd-Max centroids are off by up to
+// 0.8 of 2^-12, under the best scale by 0.09.  Values below 1/64 of the largest count
+// by their absolute error (they are left out of the choice).
+constexpr int kCentroidScales = 256;
+
+struct Centroids {
+  float c[kKvLevels], inv[kKvLevels];  // inv 0: not counted
+  float unit;                          // scale number 0
+  __device__ __forceinline__ explicit Centroids(const float* codebook) {
+    float mx = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kKvLevels; ++k) {
+      c[k] = __ldg(codebook + k);
+      mx = fmaxf(mx, fabsf(c[k]));
+    }
+    const int e = max(7, static_cast<int>(__float_as_uint(mx) >> 23));
+    unit = __uint_as_float(static_cast<uint32_t>(261 - min(e, 254)) << 23);
+#pragma unroll
+    for (int k = 0; k < kKvLevels; ++k) inv[k] = 64.0f * fabsf(c[k]) < mx || mx == 0.0f ? 0.0f : __fdividef(1.0f, c[k] * unit);
+  }
+  __device__ __forceinline__ float step(int i) const { return 1.0f + static_cast<float>(i) * (1.0f / kCentroidScales); }
+  __device__ __forceinline__ float scale(int i) const { return unit * step(i); }
+  // What the rounded centroids are of `unit` times them, on average; the return value is
+  // how far they are apart.
+  __device__ __forceinline__ float spread(int i, float& ratio) const {
+    const float s = scale(i);
+    float hi = 0.0f, lo = 4.0f;
+#pragma unroll
+    for (int k = 0; k < kKvLevels; ++k) {
+      const float r = __half2float(__float2half_rn(c[k] * s)) * inv[k];
+      hi = fmaxf(hi, r);
+      lo = fminf(lo, inv[k] == 0.0f ? lo : r);
+    }
+    ratio = 0.5f * (hi + lo);
+    return (hi - lo) * __fdividef(1.0f, step(i));
+  }
+};
+
+// The choice: one key per warp, the smallest of which (after a barrier) is it.
+template <int kThreads>
+__device__ __forceinline__ void choose_centroid_scale(const float* codebook, uint32_t* best) {
+  uint32_t key = 0xffffffffu;
+  if (threadIdx.x < kCentroidScales) {
+    const Centroids cs(codebook);
+    for (int i = threadIdx.x; i < kCentroidScales; i += kThreads) {
+      float ratio;
+      key = min(key, (__float_as_uint(fabsf(cs.spread(i, ratio))) & ~(kCentroidScales - 1u)) | static_cast<uint32_t>(i));
+    }
+  }
+  key = __reduce_min_sync(0xffffffffu, key);
+  if ((threadIdx.x & 31) == 0) best[threadIdx.x >> 5] = key;
+}
+
+// The table of binary16 pairs for two codes (one copy per lane), and in *back
+// the factor that takes a sum of its entries back; a barrier must follow.
+template <int kThreads>
+__device__ __forceinline__ void fill_centroid_table(const float* codebook, const uint32_t* best, uint32_t* table, float* back) {
+  uint32_t key = best[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) key = min(key, best[w]);
+  const Centroids cs(codebook);
+  const int n = static_cast<int>(key & (kCentroidScales - 1u));
+  const float scale = cs.scale(n);
+  if (threadIdx.x == 0) {
+    float ratio;
+    cs.spread(n, ratio);
+    *back = 1.0f / (ratio * cs.unit);
+  }
+  for (int i = threadIdx.x; i < 64 * 32; i += kThreads)
+    table[i] = pack_half2(__ldg(codebook + ((i >> 5) & 7)) * scale, __ldg(codebook + (i >> 8)) * scale);
+}
+
 // 2^x, one instruction (relative error below 2^-22; results below 2^-126 are 0).
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ float oct_max(float x) {
@@ -436,6 +512,8 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   using C = RowCfg<NT>;
   extern __shared__ __align__(16) uint8_t rsm_raw[];
   __shared__ int64_t warp_sums[kRowWarps], found[2];
+  __shared__ uint32_t best_scale[kRowWarps];
+  __shared__ float back;
   __shared__ float qmul[C::kRows];
   __shared__ float mstat[kRowWarps][C::kRows], lstat[kRowWarps][C::kRows];
   pdl_trigger();  // the join may be set up; it waits for this grid's results
@@ -449,9 +527,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   const int page_size = static_cast<int>(a.P);
 
   kv_check_codebook(a.codebook);
-  for (int i = threadIdx.x; i < 64 * 32; i += kRowThreads)
-    reinterpret_cast<uint32_t*>(gtab)[i] = pack_half2(__ldg(a.codebook + ((i >> 5) & 7)), __ldg(a.codebook + (i >> 8)));
-
+  choose_centroid_scale<kRowThreads>(a.codebook, best_scale);
   int64_t mine0;
   const int64_t U = kv_total_cost<C::kRows, kRowWinUnit, kRowItemCost, kRowThreads>(a, tiles, warp_sums, mine0);
   if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
@@ -460,6 +536,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   kv_find<C::kRows, kRowWinUnit, kRowItemCost, kRowThreads>(a, tiles, mine0, share(share.i), found);
   KvWalk<C::kRows, kRowWinUnit, kRowItemCost> w;
   w.begin(a, tiles, share, found);
+  fill_centroid_table<kRowThreads>(a.codebook, best_scale, reinterpret_cast<uint32_t*>(gtab), &back);
 
   while (w.next(a, tiles)) {
     const KvItem& it = w.it;
@@ -508,7 +585,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         const int r = 8 * nt + 2 * t4 + k;
         m[nt][k] = kMinM;
         l[nt][k] = 0.0f;
-        qm[nt][k] = qmul[r];
+        qm[nt][k] = qmul[r] * back;
         lim[nt][k] = r < nrows ? it.p + (it.row0 + r) / a.G + 1 : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[nt][i][k] = o[nt][i][2 + k] = 0.0f;
@@ -720,7 +797,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
     // ---- out of the rotated domain: O^T <- H O^T / (256 kNvScale), in registers
     if (ta < e_tb) {
-      constexpr float f = 1.0f / (256.0f * kNvScale);
+      const float f = back / (256.0f * kNvScale);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

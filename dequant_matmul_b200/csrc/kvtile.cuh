@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut* __restrict__ cuts) {
   extern __shared__ __align__(16) uint8_t asm_raw[];
   __shared__ int64_t warp_sums[kAtWarps], found[2];
+  __shared__ uint32_t best_scale[kAtWarps];
+  __shared__ float back;
   pdl_trigger();
   const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(asm_raw));
   const uint32_t tab0 = (raw + 8191u) & ~8191u;
@@ -297,6 +299,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   volatile uint32_t* misc_g = reinterpret_cast<volatile uint32_t*>(g0 + (misc - tab0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) cuts[blockIdx.x] = {0, 0, 0, 0};
+  choose_centroid_scale<kAtThreads>(a.codebook, best_scale);
   int64_t mine0;
   const int64_t U = kv_total_cost<kAtRows, kAtWinUnit, kAtItemCost, kAtThreads>(a, tiles, warp_sums, mine0);
   const KvShares share(U, blockIdx.x, gridDim.x);
@@ -306,8 +309,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
   w.begin(a, tiles, share, found);
 
   kv_check_codebook(a.codebook);
-  for (int i = threadIdx.x; i < 64 * 32; i += kAtThreads)
-    reinterpret_cast<uint32_t*>(g0)[i] = pack_half2(__ldg(a.codebook + ((i >> 5) & 7)), __ldg(a.codebook + (i >> 8)));
+  fill_centroid_table<kAtThreads>(a.codebook, best_scale, reinterpret_cast<uint32_t*>(g0), &back);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kCodeStages; ++s) {
       mbar_init(c_full + 8 * s, 1);
@@ -519,7 +521,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         float inv;
         // |q H| <= 16 |q|: with |q| brought into [16, 32) no coordinate passes 512
         const float sc = sgn * pow2_scale(sqrtf(half ? *other + ss : ss + *other), inv);
-        qm = fmaxf(fabsf(a.scale) * inv * (kLog2e / 256.0f), kMinQm);
+        qm = fmaxf(fabsf(a.scale) * inv * (kLog2e / 256.0f) * back, kMinQm);
         inv_qm = 1.0f / qm;
         across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
@@ -541,7 +543,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         // O out of the rotated domain
         within_blocks(row, half);
         pair_sync(quarter);
-        constexpr float f = 1.0f / (256.0f * kNvScale);
+        const float f = back / (256.0f * kNvScale);
         across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

@@ -722,3 +722,62 @@ def test_attention_value_norms_that_grow(hl, cb8, new, G):
         out = hl.kv_paged_attention(*args, **kw)
         torch.cuda.synchronize()
         _check(out, want, tol, new)
+
+
+# ------------------------------------------------------------------ operands of fewer bits
+def _centroid_spread(c):
+    """How far binary16 roundings of a times the levels c can agree with one common
+    factor: the best of 256 factors a between two powers of two."""
+    a = (1.0 + np.arange(256) / 256)[:, None] * np.asarray(c, np.float64)
+    r = a.astype(np.float16).astype(np.float64) / np.asarray(c, np.float64)
+    return np.min((r.max(1) - r.min(1)) / (r.max(1) + r.min(1)))
+
+
+@pytest.mark.parametrize("unit", [1.0, 2.0 ** -30, 2.0 ** 40])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_sharp_scores_of_exact_queries(hl, cb8, new, G, unit):
+    """Two keys with scores near 200 through different centroids, the others near
+    -200.  The queries have one rotated coordinate and are exact in any binary type, so
+    scores differ only by the centroids' roundings; a codebook of another unit changes
+    nothing (the norms take it back) as long as its levels are finite.
+
+    Bound: half a bf16 step of the output, 2^-8 |o|; the scores' errors e_j move o by
+    at most sum_j p_j |e_j| |v_j - o|, |e_j| <= (d + 2^-20) |s_j| with d the centroids'
+    half spread; a term of the sum has p n rounded (2^-11) and its centroids (d)."""
+    c = cb8.double().cpu().numpy()
+    d = _centroid_spread(c)
+    assert d < 0.15 * 2.0 ** -12
+    rng = np.random.default_rng(new)
+    N, P, coord = 50 + new, 16, 77
+    i = np.arange(N)
+    codes = rng.integers(0, 8, (2, N, 256))
+    codes[0, :, coord] = rng.integers(0, 4, N)
+    pair = [3, 45]
+    codes[0, pair, coord] = [5, 7]
+    s = np.full(N, 200.0)
+    s[pair] += [0.2, -0.3]
+    norms = np.stack([(s * 16 / (4 * np.abs(c[codes[0, :, coord]]))), np.full(N, 20.0)]).astype(np.float16)
+    s = 4 * norms[0].astype(np.float64) * c[codes[0, :, coord]] / 16          # the query is 4 (H256)_coord
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    had = np.array([[1.0]])
+    while had.shape[0] < 256:
+        had = np.block([[had, had], [had, -had]])
+    V = c[codes[1]] @ had * norms[1].astype(np.float64)[:, None] / 256
+    want = w @ V
+    size = np.linalg.norm(V, axis=1)
+    tol = 2.0 ** -8 * np.linalg.norm(want) + (w * ((d + 2.0 ** -20) * np.abs(s) * np.linalg.norm(V - want, axis=1)
+                                                   + (2.0 ** -11 + d) * size)).sum()
+    pages = -(-N // P)
+    dev = []
+    for which in range(2):
+        packed, nr = np.zeros((pages, 1, P, 96), np.uint8), np.zeros((pages, 1, P), np.float16)
+        packed[i // P, 0, i % P] = O.pack_codes(codes[which], bits=3)
+        nr[i // P, 0, i % P] = norms[which]
+        dev.append(_dev_pages(packed, nr))
+    Q = torch.from_numpy(np.broadcast_to(4 * had[coord], (new, G, 256)).copy()).to(torch.bfloat16)
+    out = hl.kv_paged_attention((Q.double() / unit).to(torch.bfloat16).cuda(), _ints([0, new]), _ints([N - new]),
+                                _ints(np.arange(pages)[None]), *dev, None, (cb8.double() * unit).float(), new)
+    torch.cuda.synchronize()
+    err = np.linalg.norm(out.double().cpu().numpy() / unit - want, axis=-1)
+    assert np.all(err <= tol), (err.max() / tol)
