@@ -231,10 +231,12 @@ struct KvWalk {
 
 // ---------------------------------------------------------------- building blocks
 
-// 2^k that brings a row's largest magnitude (>= 0) into [16, 32); 1 for a zero row.
+// 2^k that brings the largest magnitude mx of a row of Q into [64, 128), so that no
+// coordinate of the rotated row passes 128 * 256 = 2^15; 1 for a zero row.  (The power of
+// the smallest rows stays below 2^118: 512 times it is finite.)
 __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
   const int e = static_cast<int>(__float_as_uint(mx) >> 23);
-  const int k = e == 0 ? 0 : max(-120, min(120, 131 - e));
+  const int k = e == 0 ? 0 : max(-126, min(117, 133 - e));
   inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
@@ -435,7 +437,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // does not see or gives no weight.  O^T's registers hold 32 consecutive dims of two
 // rows: the rotation back is five in-register and three shuffle stages.  The window's
 // keys come after it and are multiplied as they are, un-rotated bf16 with the
-// query's own bits.
+// query's own bits (times a power of two).
 //
 // Bound: HBM by its bytes (196 per token and kv head); in fact integer instructions
 // and shared-memory reads, one warp instruction in five a table read.  64 requests
@@ -554,7 +556,13 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       float v[32];
       load_bf16x32(v, a.q + static_cast<int64_t>(it.c0 + tok) * a.ldq + (h * a.G + (row - tok * a.G)) * kKvDim + 32 * l8, on);
       const uint32_t dst = qfrag + ((r >> 3) * 16 * 32 + (r & 7) * 4 + (l8 >> 1)) * 8 + (l8 & 1) * 8 * 256;
-      // as it is (for the window's keys), its bf16 bits exact
+      float mx = 0.0f, inv;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
+      const float sc = pow2_scale(oct_max(mx), inv);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] *= sc;
+      // not rotated (for the window's keys): its bf16 bits, another exponent
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + C::kQFrag + s * 256),
@@ -562,16 +570,11 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
                      "r"(__byte_perm(__float_as_uint(v[4 * s + 2]), __float_as_uint(v[4 * s + 3]), 0x7632))
                      : "memory");
       kv_fwht(v, lane);
-      float mx = 0.0f, inv;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
-      const float sc = pow2_scale(oct_max(mx), inv);
       if (l8 == 0) qmul[r] = inv * a.scale * (kLog2e / 256.0f);
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + s * 256),
-                     "r"(pack_half2(v[4 * s] * sc, v[4 * s + 1] * sc)),
-                     "r"(pack_half2(v[4 * s + 2] * sc, v[4 * s + 3] * sc))
+                     "r"(pack_half2(v[4 * s], v[4 * s + 1])), "r"(pack_half2(v[4 * s + 2], v[4 * s + 3]))
                      : "memory");
     }
     __syncthreads();
@@ -826,7 +829,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     const int w_end = min(it.e_lim + (tb - it.e_units) * kRowWinUnit, it.w_lim);
     if (w_first < w_end) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) qm[nt][0] = qm[nt][1] = a.scale * kLog2e;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) qm[nt][k] = 256.0f * qmul[8 * nt + 2 * t4 + k];
     }
 #pragma unroll 1
     for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {

@@ -66,7 +66,7 @@ constexpr int kMaskOff = kNormOff + 256;
 constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
 constexpr int kNrmSlot = 192 * 4 + 16;               // K norms, V norms (kNvScale times), log2_above of V's, mask
 constexpr int kSlotMask = 192 * 4;
-constexpr float kMinQm = 1e-36f;                     // a zero scale: masked keys (-inf) stay masked, the others equal
+constexpr float kMinQm = 1e-36f;                     // encoded scores of less are 0; log2_above / kMinQm is finite
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 constexpr int kAtSmem = 8192 /*align*/ + 8192 /*table*/ + 4 * kKvTile + kCodeStages * kCodeStage + 4 * kNrmSlot + 512 +
                         2 * kAtRows * 4 /*row exchange*/;
@@ -342,7 +342,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     // ------------------------------------------------------------ softmax
     const int half = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;  // r: row of the tile
     const uint32_t row = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const float sgn = a.scale < 0.0f ? -1.0f : 1.0f;
+    const float sgn = a.scale < 0.0f ? -1.0f : a.scale > 0.0f ? 1.0f : 0.0f;  // a zero scale: Q is 0, qm is not
     float* mine = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + half * kAtRows + r;       // exchange with the
     const float* other = reinterpret_cast<float*>(g0 + (bars + 512 - tab0)) + (half ^ 1) * kAtRows + r;  // row's other thread
     uint32_t gt = 0;
@@ -361,6 +361,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       // m: the row's reference, which follows its largest p n as in the few-row
       // kernel; l: this thread's share of the row's sum
       float m = kMinM, l = 0.0f, qm = 0.0f, inv_qm = 0.0f;
+      float q_inv = 0.0f;    // what takes the row's power of two back (0: not looked for yet)
       bool started = false;  // O holds something
 
       // One tile: S(gt) -> P(gt).  win: window keys, p in two bf16 parts.  This
@@ -498,7 +499,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       if (w.ta < w.e_tb) {
         // Q, rotated: this thread's two blocks of 64 dims, then its columns across
         // the blocks, into binary16
-        float ss = 0.0f;
+        float mx = 0.0f;
 #pragma unroll 1
         for (int c = 2 * half; c < 2 * half + 2; ++c) {
           float v[64];
@@ -511,17 +512,18 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             for (int k = 0; k < 4; ++k) v[8 * i + 2 * k] = bf16x2_lo(xs[k]), v[8 * i + 2 * k + 1] = bf16x2_hi(xs[k]);
           }
 #pragma unroll
-          for (int i = 0; i < 64; ++i) ss = fmaf(v[i], v[i], ss);
+          for (int i = 0; i < 64; ++i) {
+            mx = fmaxf(mx, fabsf(v[i]));
+            v[i] *= 1.0f / 512.0f;  // no sum of 256 values overflows
+          }
           fwht64(v);
           tc_st64(row + kColO + 64 * c, v);
         }
         tc_wait_st();
-        *mine = ss;
+        *mine = mx;
         pair_sync(quarter);
-        float inv;
-        // |q H| <= 16 |q|: with |q| brought into [16, 32) no coordinate passes 512
-        const float sc = sgn * pow2_scale(sqrtf(half ? *other + ss : ss + *other), inv);
-        qm = fmaxf(fabsf(a.scale) * inv * (kLog2e / 256.0f) * back, kMinQm);
+        const float sc = sgn * 512.0f * pow2_scale(fmaxf(mx, *other), q_inv);
+        qm = sgn == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * q_inv * (kLog2e / 256.0f) * back, kMinQm);
         inv_qm = 1.0f / qm;
         across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
@@ -556,7 +558,23 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         pair_sync(quarter);
       }
       if (w.e_tb < w.tb) {
-        // window units: Q as it is
+        // window units: Q not rotated, its bf16 bits with another exponent
+        if (q_inv == 0.0f) {
+          __nv_bfloat162 mx = __float2bfloat162_rn(0.0f);
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (on) y = __ldg(reinterpret_cast<const uint4*>(qrow + 128 * half) + i);
+            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = __hmax2(mx, __habs2(p[k]));
+          }
+          const float2 f = __bfloat1622float2(mx);
+          *mine = fmaxf(f.x, f.y);
+          pair_sync(quarter);
+          pow2_scale(fmaxf(fmaxf(f.x, f.y), *other), q_inv);
+        }
+        const __nv_bfloat162 sc = __float2bfloat162_rn(sgn / q_inv);
 #pragma unroll 1
         for (int c = 4 * half; c < 4 * half + 4; ++c) {
           uint32_t x[16];
@@ -564,13 +582,17 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           for (int i = 0; i < 4; ++i) {
             uint4 y = make_uint4(0u, 0u, 0u, 0u);
             if (on) y = __ldg(reinterpret_cast<const uint4*>(qrow + 32 * c) + i);
-            const uint32_t flip = sgn < 0.0f ? 0x80008000u : 0u;
-            x[4 * i] = y.x ^ flip, x[4 * i + 1] = y.y ^ flip, x[4 * i + 2] = y.z ^ flip, x[4 * i + 3] = y.w ^ flip;
+            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 z = __hmul2(p[k], sc);
+              x[4 * i + k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
           }
           tc_st16(row + kColQ + 16 * c, x);
         }
         tc_wait_st();
-        qm = fmaxf(fabsf(a.scale) * kLog2e, kMinQm);
+        qm = sgn == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * q_inv * kLog2e, kMinQm);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);

@@ -781,3 +781,16 @@ def test_attention_sharp_scores_of_exact_queries(hl, cb8, new, G, unit):
     torch.cuda.synchronize()
     err = np.linalg.norm(out.double().cpu().numpy() / unit - want, axis=-1)
     assert np.all(err <= tol), (err.max() / tol)
+
+
+@pytest.mark.parametrize("e", [-110, -70, 50, 70, 100, 122])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_query_magnitudes(hl, cb8, new, G, e):
+    """Queries 2^e times as large under a scale 2^-e times as large give the same scores:
+    powers of two, so the same tolerance holds."""
+    X, Y, Q = _rows(90, 1, 80, False), _rows(90, 1, 81, False), _rows(new, G, 82, False)
+    for R in (0, 30):
+        args, kw, want, tol = _attend_on(hl, cb8, X, Y, Q, new, R, G)
+        out = hl.kv_paged_attention((Q.double() * 2.0 ** e).to(torch.bfloat16).cuda(), *args[1:], scale=2.0 ** (-4 - e), **kw)
+        torch.cuda.synchronize()
+        _check(out, want, tol, new)
