@@ -42,7 +42,7 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Pages of the encoded tokens among n (R slots of window, P tokens to a page).
-__device__ __forceinline__ uint32_t kv_pages(uint32_t n, uint32_t R, uint32_t P) { return n > R ? (n - R + P - 1) / P : 0u; }
+__device__ __forceinline__ uint32_t kv_pages(uint32_t n, uint32_t R, uint32_t P) { return n > R ? (n - R - 1) / P + 1 : 0u; }
 
 constexpr uint32_t kTabCap = 0x3fffffffu;  // sums saturate here: two of them still add in 32 bits
 
@@ -111,11 +111,11 @@ kv_tables_kernel(const int32_t* __restrict__ n_past, const int32_t* __restrict__
     uint32_t n = 0, need = 0;
     if (b < B) {  // negative lengths count as 0
       const int p = __ldg(n_past + b), m = __ldg(n_new + b);
-      bad |= p < 0 || m < 0;
       const uint32_t up = max(p, 0), un = max(m, 0);
+      bad |= p < 0 || m < 0 || up + un > static_cast<uint32_t>(INT32_MAX);
       const uint32_t old = kv_pages(up, R, P), want = kv_pages(up + un, R, P);
       full |= want > max_pages;
-      need = min(want, max_pages) - min(old, max_pages);
+      need = min(min(want, max_pages) - min(old, max_pages), kTabCap);
       n = min(un, kTabCap);
     }
     uint32_t ta, tb;

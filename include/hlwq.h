@@ -242,7 +242,8 @@ int hlwq_kv_scores_window(const uint16_t* q, int64_t m, int64_t ldq, const uint8
  *   entries of pages in use are read only.  A page that is not to be had (the
  *   pool is empty, or the row of max_pages is full) raises
  *   HLWQ_DEVERR_KV_PAGES; its entry and slots are -1.  Negative lengths count
- *   as 0 and, like sum n_new > T, raise HLWQ_DEVERR_KV_RANGE.
+ *   as 0 and, like sum n_new > T and n_past + n_new >= 2^31, raise
+ *   HLWQ_DEVERR_KV_RANGE.
  * hlwq_kv_paged_append: encodes every token that leaves (from its ring slot,
  *   or from K / V when the chunk is longer than the window) into its slot,
  *   codes and norms as those of hlwq_kv_quantize, and copies the new tokens

@@ -794,3 +794,28 @@ def test_attention_query_magnitudes(hl, cb8, new, G, e):
         out = hl.kv_paged_attention((Q.double() * 2.0 ** e).to(torch.bfloat16).cuda(), *args[1:], scale=2.0 ** (-4 - e), **kw)
         torch.cuda.synchronize()
         _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("R,P", [(0, 16), (3, 64), (128, 4096)])
+def test_block_tables_with_lengths_whose_sum_is_near_2_32(hl, R, P):
+    """Such a request is reported and gets no page; the others' pages are what they are without it."""
+    hl.device_error()
+    top = 2 ** 31 - 1
+    past, new, width = [5, top, 40], [2 * P, top, R + 3 * P], 6
+    table = np.full((3, width), -1)
+    table[1] = range(20, 26)
+    for b in (0, 2):
+        k = O.kv_pages(past[b], P, R)
+        table[b, :k] = range(30 + b * 6, 30 + b * 6 + k)
+    free, T = list(range(12)), 2 * P + 3
+    want = O.kv_block_tables(past, [new[0], 0, new[2]], free, table, P, R, T)
+    t = _ints(table)
+    cu, slots, left = hl.kv_block_tables(_ints(past), _ints(new), _ints(free), _ints([12]), t, P, R, T)
+    torch.cuda.synchronize()
+    assert hl.device_error() & hl.DEVERR_KV_RANGE
+    assert np.array_equal(t.cpu().numpy(), want[0]) and int(left) == want[3]
+    assert np.array_equal(slots[:2 * P].cpu().numpy(), want[2][:2 * P])
+    # just below the limit: nothing to report about the length itself
+    hl.kv_block_tables(_ints([top - 3]), _ints([3]), _ints(free), _ints([12]), torch.full((1, width), -1, dtype=torch.int32, device="cuda"),
+                       P, R, 3)
+    assert hl.device_error() == hl.DEVERR_KV_PAGES
