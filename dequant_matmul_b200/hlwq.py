@@ -8,6 +8,7 @@ be loaded the import fails loudly -- there is no fallback implementation.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -602,17 +603,22 @@ class PagedKVCache:
             self.n_past += self.n_new
             self.n_free.copy_(self._n_free_next)
 
-    def release(self, b: int):
-        """Empties request row b between two steps and gives its pages back
-        (reads its length: synchronises)."""
-        k = -(-max(0, int(self.n_past[b]) - self.R) // self.page_size)
-        pages = self.block_table[b, :k]
-        pages = pages[pages >= 0]  # an exhausted pool leaves -1 in the table
-        n, k = int(self.n_free), pages.numel()
-        self.free_pages[n:n + k] = pages
-        self.n_free += k
-        self.block_table[b] = -1
-        self.n_past[b] = 0
+    def release(self, b: int, stream=None):
+        """Empties request row b between two steps and gives its pages back, on the
+        stream of the steps (reads the row's length: waits for that stream)."""
+        if self.n_past.is_cuda:
+            on = torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.n_past.device))
+        else:
+            on = contextlib.nullcontext()
+        with on:
+            k = -(-max(0, int(self.n_past[b]) - self.R) // self.page_size)
+            pages = self.block_table[b, :k]
+            pages = pages[pages >= 0]  # an exhausted pool leaves -1 in the table
+            n, k = int(self.n_free), pages.numel()
+            self.free_pages[n:n + k] = pages
+            self.n_free += k
+            self.block_table[b] = -1
+            self.n_past[b] = 0
 
 
 def gemv(packed, norms, cb, x: torch.Tensor, out_dtype=torch.float32, y=None, stream=None, flags: int = 0):

@@ -819,3 +819,28 @@ def test_block_tables_with_lengths_whose_sum_is_near_2_32(hl, R, P):
     hl.kv_block_tables(_ints([top - 3]), _ints([3]), _ints(free), _ints([12]), torch.full((1, width), -1, dtype=torch.int32, device="cuda"),
                        P, R, 3)
     assert hl.device_error() == hl.DEVERR_KV_PAGES
+
+
+def test_release_on_the_stream_of_the_steps(hl, cb8):
+    """Steps and a release between them on a side stream that is far behind the host, without
+    a synchronisation of the device: no page is lost or given out twice."""
+    H, P, B = 1, 16, 3
+    cache = hl.PagedKVCache(B, H, num_pages=12, max_pages=12, page_size=P, R=0, cb8=cb8)
+    x = _rows(120, H, 9).cuda()
+    news = [_ints(v) for v in ([70, 40, 0], [0, 1, 60])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    for k, n_new in enumerate(news):
+        T = int(sum(([70, 40, 0], [0, 1, 60])[k]))
+        cache.begin(n_new, T, stream=side)
+        cache.append(x[:T], x[:T], stream=side)
+        cache.end(stream=side)
+        if k == 0:
+            cache.release(0, stream=side)
+    side.synchronize()
+    assert cache.n_past.tolist() == [0, 41, 60] and int(cache.n_free) == 12 - 3 - 4
+    held = [p for row in cache.block_table.tolist() for p in row if p >= 0]
+    assert sorted(held + cache.free_pages[:5].tolist()) == list(range(12))
+    assert hl.device_error() == 0
