@@ -557,7 +557,12 @@ class PagedKVCache:
         cache.begin(n_new, T)        # int32 [B] on the device; rows of K, V, Q
         cache.append(K, V)
         out = cache.attention(Q, max_new)
-        cache.end()                  # n_new joins n_past
+        cache.end()                  # the step's tokens join n_past
+
+    All tokens of a step stay: there is no way to take back rejected drafts.  The
+    append has overwritten the ring slots of the tokens that would belong to the window
+    again, and the tables hold the drafts' pages.  Neither n_new (read by begin
+    alone) nor n_past may be lowered for it; release() empties a whole row.
     """
 
     def __init__(self, requests: int, kv_heads: int, num_pages: int, max_pages: int, page_size: int = 64, R: int = 128,
@@ -600,7 +605,7 @@ class PagedKVCache:
 
     def end(self, stream=None):
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.n_past.device)):
-            self.n_past += self.n_new
+            self.n_past += self.cu_new[1:] - self.cu_new[:-1]  # the lengths that begin() took
             self.n_free.copy_(self._n_free_next)
 
     def release(self, b: int, stream=None):

@@ -234,6 +234,11 @@ int hlwq_kv_scores_window(const uint16_t* q, int64_t m, int64_t ldq, const uint8
  *                  token's heads are contiguous, ldk / ldv / ldq / ldo elements
  *                  from token to token
  *
+ * All tokens of a step stay.  n_past must not be lowered afterwards (to take
+ * rejected drafts back, say): the append has overwritten the ring slots of the
+ * tokens that would be in the window again, and pages that the table holds for
+ * the tokens taken back would be taken from the pool a second time.
+ *
  * hlwq_kv_block_tables: cu_new, slot_map and the block-table entries of the
  *   pages that this step needs first.  Pages come from the stack free_pages
  *   [free_cap], whose entries [0, n_free[0]) are free, last entry first, in

@@ -844,3 +844,26 @@ def test_release_on_the_stream_of_the_steps(hl, cb8):
     held = [p for row in cache.block_table.tolist() for p in row if p >= 0]
     assert sorted(held + cache.free_pages[:5].tolist()) == list(range(12))
     assert hl.device_error() == 0
+
+
+@pytest.mark.parametrize("R", [0, 8])
+def test_the_step_ends_with_the_lengths_it_began_with(hl, cb8, R):
+    """n_new lowered after the append (as if drafts were rejected) does not make appended tokens
+    older ones, and a negative length counts as 0 to the end."""
+    hl.device_error()
+    H, G, N = 1, 4, 26
+    X, Y, Q = _rows(N, H, 1), _rows(N, H, 2), _rows(N, G, 3, False)
+    cache = hl.PagedKVCache(2, H, num_pages=8, max_pages=8, page_size=16, R=R, cb8=cb8)
+    for lo, n in ((0, 20), (20, 5), (25, 1)):
+        n_new = _ints([n, -3])
+        cache.begin(n_new, n)
+        cache.append(X[lo:lo + n].cuda(), Y[lo:lo + n].cuda())
+        out = torch.full((n, G, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+        cache.attention(Q[lo:lo + n].cuda(), n, out=out)
+        n_new[0] = 2
+        cache.end()
+        assert cache.n_past.tolist() == [lo + n, 0]
+        assert hl.device_error() == hl.DEVERR_KV_RANGE   # the negative length
+        want, tol = _reference(X[:lo + n], Y[:lo + n], Q[lo:lo + n], lo + n, n, R, G)
+        _check(out, want, tol, n)
+    assert int(cache.n_free) == 8 - O.kv_pages(N, 16, R)
