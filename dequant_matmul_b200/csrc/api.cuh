@@ -310,10 +310,10 @@ extern "C" int hlwq_kv_paged_attention(const uint16_t* Q, int64_t ldq, int64_t T
   const size_t need = hlwq_workspace_bytes(HLWQ_OP_KV_ATTENTION, T, max_new, B, q_heads, kv_heads);
   if (need && (!workspace || ws_bytes < need)) return HLWQ_EWORKSPACE;
   if (need && !aligned16(workspace)) return HLWQ_EALIGN;
-  const hlwq::KvAttn a{Q, out, ldq, ldo, T, cu_new, n_past, static_cast<int>(B), static_cast<int>(q_heads),
+  const hlwq::KvAttn a{Q, out, ldq, ldo, T, max_new, cu_new, n_past, static_cast<int>(B), static_cast<int>(q_heads),
                        static_cast<int>(kv_heads), static_cast<int>(q_heads / kv_heads), scale, codebook8, k_packed,
                        k_norms, v_packed, v_norms, num_pages, page_size, block_table, max_pages, k_window, v_window, R};
-  return hlwq::launch_kv_attention(a, max_new, workspace, ws_bytes, as_stream(stream));
+  return hlwq::launch_kv_attention(a, workspace, ws_bytes, as_stream(stream));
 }
 
 extern "C" int hlwq_gemv(const uint8_t* packed, const uint16_t* norms, const float* codebook, int64_t out,

@@ -22,7 +22,7 @@ namespace {
 struct KvAttn {
   const uint16_t* q;
   uint16_t* out;
-  int64_t ldq, ldo, T;
+  int64_t ldq, ldo, T, max_new;
   const int32_t* cu;
   const int32_t* n_past;
   int B, Hq, H, G;
@@ -88,7 +88,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, 
     return it;
   }
   const int rows = it.n * a.G;
-  if (rt == 0 && rows > tiles * kRows) bad = true;  // more than max_new tokens
+  if (n > a.max_new) bad = true;  // (the rows past the last tile have no item)
   it.row0 = rt * kRows;
   it.nrows = min(kRows, rows - it.row0);
   if (it.nrows <= 0) return it;

@@ -935,8 +935,8 @@ size_t kv_attention_workspace_bytes(int64_t, int64_t max_new, int64_t, int64_t H
   return static_cast<size_t>(gr.ctas) * (2 * gr.rows * (kKvDim + 2) * sizeof(float) + sizeof(KvCut));
 }
 
-int launch_kv_attention(const KvAttn& a, int64_t max_new, void* workspace, size_t, cudaStream_t stream) {
-  const KvGrid gr = kv_grid(max_new, a.G);
+int launch_kv_attention(const KvAttn& a, void* workspace, size_t, cudaStream_t stream) {
+  const KvGrid gr = kv_grid(a.max_new, a.G);
   if (gr.tiles * a.B > INT32_MAX) return HLWQ_EUNSUPPORTED;
   const int tiles = static_cast<int>(gr.tiles);
   float* parts = static_cast<float*>(workspace);

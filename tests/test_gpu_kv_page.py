@@ -867,3 +867,18 @@ def test_the_step_ends_with_the_lengths_it_began_with(hl, cb8, R):
         want, tol = _reference(X[:lo + n], Y[:lo + n], Q[lo:lo + n], lo + n, n, R, G)
         _check(out, want, tol, n)
     assert int(cache.n_free) == 8 - O.kv_pages(N, 16, R)
+
+
+@pytest.mark.parametrize("max_new,new,G", [(2, 3, 2), (1, 2, 8), (7, 8, 2), (100, 120, 1), (100, 101, 6), (20, 300, 6)])
+def test_attention_more_tokens_than_max_new(hl, cb8, max_new, new, G):
+    """Reported whether or not the rows still fit the last row tile; the other request's
+    rows are right, and so are the rows that were written."""
+    hl.device_error()
+    args, kw, want, tol = _attend(hl, cb8, [30, 50], [1, new], 1, G, 16, 8, seed=13, max_new=max_new)
+    out = hl.kv_paged_attention(*args, **kw)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
+    written = 1 + max_new
+    err = np.linalg.norm(out[:written].double().cpu().numpy() - want[:written], axis=-1)
+    assert np.all(err <= tol[:written])
+    hl.kv_paged_attention(*args[:-1], new, **kw)
+    assert hl.device_error() == 0
