@@ -274,6 +274,13 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
   __shared__ double mid[kKvLevels - 1];
   __shared__ __align__(16) uint8_t swaps[kAppThreads / 32][4 * 4 * kKvDim];      // rotated vectors
   __shared__ __align__(16) uint8_t stages[kAppThreads / 32][kAppStages * kAppStage];  // vectors under way
+  // every request's rows and length, by all threads (those with nothing to append would
+  // not be looked at otherwise)
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kAppThreads + threadIdx.x; r < B;
+       r += static_cast<int64_t>(gridDim.x) * kAppThreads) {
+    const int from_row = __ldg(cu + r), to_row = __ldg(cu + r + 1), past = __ldg(n_past + r);
+    if (from_row < 0 || to_row < from_row || to_row > T || past < 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
+  }
   kv_check_codebook(codebook);
   if (threadIdx.x < kKvLevels - 1)
     mid[threadIdx.x] = 0.5 * (static_cast<double>(__ldg(codebook + threadIdx.x)) +
@@ -288,7 +295,6 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kAppThreads + threadIdx.x) >> 5;
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kAppThreads / 32);
   const int64_t end = min(T, static_cast<int64_t>(__ldg(cu + B)));
-  if (__ldg(cu + B) > T && blockIdx.x == 0 && threadIdx.x == 0) raise_device_error(HLWQ_DEVERR_KV_RANGE);
   const int toks = H == 1 ? 2 : 1, groups = H == 1 ? 1 : (H + 1) / 2;  // tokens of a step, warps side by side
   const int lanes = static_cast<int>(nwarps / groups);                 // warps along the tokens
   const int group = static_cast<int>(warp % groups);
@@ -327,7 +333,7 @@ kv_append_kernel(const uint16_t* __restrict__ K, int64_t ldk, const uint16_t* __
       next = __ldg(cu + b + 1);
       p = __ldg(n_past + b);
       live = c0 >= 0 && t >= c0 && t < next && next <= T && p >= 0;
-      if (!live) {
+      if (!live) {  // (reported above, unless t is ahead of the first request)
         raise_device_error(HLWQ_DEVERR_KV_RANGE);
         next = t + 1;
       }

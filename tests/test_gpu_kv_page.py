@@ -882,3 +882,35 @@ def test_attention_more_tokens_than_max_new(hl, cb8, max_new, new, G):
     assert np.all(err <= tol[:written])
     hl.kv_paged_attention(*args[:-1], new, **kw)
     assert hl.device_error() == 0
+
+
+# Offsets that are not those of requests in [0, T), and negative lengths (T = 3 rows).
+BAD_STEPS = [([0, 4], [0]), ([0, 9], [0]), ([2, 1], [0]), ([2, 0], [0]), ([-1, 2], [0]), ([0, 3], [-1]), ([0, 0], [-5]),
+             ([0, 2, 1], [0, 0]), ([0, 3, 2], [0, 0]), ([0, 1, 3], [0, -2]), ([0, 0, 3], [-1, 0])]
+
+
+@pytest.mark.parametrize("cu,past", BAD_STEPS)
+def test_append_reports_rows_out_of_range(hl, cb8, cu, past):
+    """Always, whether or not the request has a token; places of no slot stay as they are."""
+    hl.device_error()
+    pages = [(torch.zeros(2, 1, 16, 96, dtype=torch.uint8, device="cuda"),
+              torch.zeros(2, 1, 16, dtype=torch.uint16, device="cuda")) for _ in range(2)]
+    x = _rows(3, 1, 5).cuda()
+    hl.kv_paged_append(x, x, _ints([4, 5, 6], torch.int64), _ints(cu), _ints(past), *pages, None, cb8)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
+    for p, n in pages:
+        assert set(n.view(torch.int16).reshape(-1).nonzero().flatten().tolist()) <= {4, 5, 6}
+    hl.kv_paged_append(x, x, _ints([4, 5, 6], torch.int64), _ints([0, 3]), _ints([0]), *pages, None, cb8)
+    assert hl.device_error() == 0
+
+
+@pytest.mark.parametrize("cu,past", BAD_STEPS)
+@pytest.mark.parametrize("max_new", [1, 40])
+def test_attention_reports_rows_out_of_range(hl, cb8, cu, past, max_new):
+    hl.device_error()
+    T, G = 3, 4
+    args, kw, want, tol = _attend(hl, cb8, [20, 30], [2, 1], 1, G, 16, 0, seed=8, behind=0)
+    if len(past) == 1:
+        args = (args[0], args[1], args[2], args[3][:1], *args[4:])
+    hl.kv_paged_attention(args[0], _ints(cu), _ints(past), *args[3:-1], max(3, max_new), **kw)
+    assert hl.device_error() == hl.DEVERR_KV_RANGE
