@@ -274,7 +274,9 @@ int hlwq_kv_scores_window(const uint16_t* q, int64_t m, int64_t ldq, const uint8
  * max_new <= 0; T > 2^30; R < 0 or > 2^20; q_heads not a multiple of kv_heads;
  * ld below heads * 256; n_free_out == n_free; scale not finite),
  * HLWQ_EUNSUPPORTED (page_size not a multiple of 16 in 16 .. 4096; B > 8192;
- * q_heads / kv_heads > 64; kv_heads > 1024; T * q_heads >= 2^31), HLWQ_EALIGN (packed, norms,
+ * q_heads / kv_heads > 64; kv_heads > 1024; T * q_heads >= 2^31; B times the
+ * row tiles of max_new tokens, min(max_new, T) * q_heads / kv_heads / 128 rounded
+ * up, >= 2^31), HLWQ_EALIGN (packed, norms,
  * windows, K, V, Q, out and workspace 16-byte, ld a multiple of 8 elements,
  * int32 arrays 4-byte, slot_map 8-byte), HLWQ_EWORKSPACE, HLWQ_ECUDA.
  */

@@ -184,3 +184,14 @@ def test_release_gives_back_the_pages_that_there_are(hl):
     cache.release(0)                                         # an empty row
     cache.release(1)
     assert int(cache.n_free) == 8 and sorted(cache.free_pages.tolist()) == list(range(8))
+
+
+def test_attention_refuses_too_many_row_tiles(hl):
+    """B times the row tiles of max_new tokens has to stay below 2^31, whatever the lengths are."""
+    T, G, B = 1 << 24, 64, 8192
+    ws = hl.workspace_bytes(hl.HLWQ_OP_KV_ATTENTION, T, T, B, G, 1)
+    args = dict(Q=P16, ldq=G * 256, T=T, Hq=G, H=1, scale=0.0625, cu=P16, n_past=P16, B=B, max_new=T, table=P16, max_pages=8,
+                cb=P16, kp=P16, kn=P16, vp=P16, vn=P16, num_pages=10, P=64, kw=P16, vw=P16, R=128, out=P16, ldo=G * 256,
+                ws=P16, ws_bytes=ws, stream=None)
+    assert B * (T * G // 128) >= 2 ** 31
+    assert hl.lib.hlwq_kv_paged_attention(*args.values()) == hl.HLWQ_EUNSUPPORTED
