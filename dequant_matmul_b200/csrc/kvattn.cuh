@@ -433,20 +433,27 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // raised only when one exceeds it by 8 (in powers of two), so most steps need no exchange
 // between lanes.  Then p n < 2^8 (p itself, at most 2^22, is summed in fp32), and kNvScale
 // brings it to where binary16 has 11 bits for it down to 2^-20 of the row's largest
-// term and to 2^-31 of that term below, whatever the norms of keys are that the row
-// does not see or gives no weight.  O^T's registers hold 32 consecutive dims of two
+// term (of a norm from 2^-14 up) and steps of 2^-30 of that term below, whatever the
+// norms of keys are that the row does not see or gives no weight.  O^T's registers hold 32 consecutive dims of two
 // rows: the rotation back is five in-register and three shuffle stages.  The window's
 // keys come after it and are multiplied as they are, un-rotated bf16 with the
 // query's own bits (times a power of two).
 //
+// Fewer than 32 bits: the rotated query has 11 per coordinate (the query came with 8), p n
+// has 11, the centroids about 14 (above).  Their products are exact and are summed in
+// fp32.  With scores of up to 65 over 4000 keys the query's part moves the output by
+// 0.1 in a thousand in the median and by up to 3 in a thousand, the other two by up to
+// 0.3; half a step of the bf16 output is 2 to 4 in a thousand.  The query in two binary16 parts (22 bits)
+// was built: 64 requests 214 us instead of 165, one of 131071 tokens 78 instead of 65.
+//
 // Bound: HBM by its bytes (196 per token and kv head); in fact integer instructions
 // and shared-memory reads, one warp instruction in five a table read.  64 requests
-// of 64 to 16384 tokens, 4 kv heads of 6 rows (438 MB): 166 us, 2.6 TB/s, DRAM
+// of 64 to 16384 tokens, 4 kv heads of 6 rows (438 MB): 163 us, 2.7 TB/s, DRAM
 // traffic equal to the bytes, 730 warp instructions per 16 keys at 2.3 per cycle
-// (ALU pipe 57 %, shared memory 57 %).  A tcgen05 kernel would have to write the decoded
+// (ALU pipe 59 %, shared memory 57 %).  A tcgen05 kernel would have to write the decoded
 // tiles to shared memory first, as much traffic again as the table reads; the
 // legacy instruction takes them from registers, and with 8 or 16 rows its
-// rate is no limit (tensor pipe 20 %).
+// rate is no limit (tensor pipe 21 %).
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;

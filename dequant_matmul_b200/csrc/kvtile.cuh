@@ -30,9 +30,14 @@
 // rows is the same key; P's columns follow by picking registers.  The 16-key
 // groups of a stage are 16 bytes further apart than their contents for the same reason.
 //
+// Fewer than 32 bits: as in the few-row kernel (query and p n 11 bits, centroids about
+// 14).  A second part of the query has no room: O, Q and the two S tiles fill the tensor
+// memory, and of shared memory 42 of the 64 KB that it takes are free.
+//
 // What bounds it, per tile of 64 keys (about 2900 cycles; the matrix work is 1024):
 // the softmax warps, busy for some 2500 cycles from S(j) to P(j) (tensor-memory
-// reads, norms, 8192 exponentials at 16 per cycle, packing), close to the decoders' 2250
+// reads, norms and their logarithms, 8192 exponentials at 16 per cycle, packing; the
+// logarithms, which let the reference follow p n, are 2 % of the time), close to the decoders' 2250
 // and to shared memory, whose 128 bytes per cycle are busy four fifths of the time
 // (table reads and tile stores 1000 cycles, staging and norms 300, the MMAs' B
 // operands 512).  Tried and slower: four threads per row (1.07 times the time),
@@ -916,7 +921,13 @@ int launch_tiles(const KvAttn& a, int ctas, int tiles, float* parts, KvCut* cuts
 }
 
 // Rows per tile, CTAs, and row tiles of a request for max_new new tokens: the
-// few-row kernel up to 16 rows per kv head, the tensor-core tiles above.
+// few-row kernel up to 16 rows per kv head, the tensor-core tiles above.  Measured, us
+// for 16 requests of 100 to 7000 tokens and 8 kv heads / one of 60000 tokens and 4:
+//   rows              8           12           16           18           24           32           48
+//   tiles of 8     75 / 50    103 / 60     103 / 60     137 / 73     143 / 75     169 / 89     298 / 118
+//   tiles of 16    91 / 58     91 / 60      91 / 60     145 / 71     146 / 73     149 / 73     239 / 103
+//   tiles of 128  132 / 89    124 / 97     126 / 93     128 / 97     126 / 93     124 / 91     157 / 93
+// (One request alone would do better on two tiles of 16 up to 32 rows; batches would not.)
 struct KvGrid {
   int rows, ctas;
   int64_t tiles;

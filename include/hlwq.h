@@ -256,16 +256,24 @@ int hlwq_kv_scores_window(const uint16_t* q, int64_t m, int64_t ldq, const uint8
  *   step.  A token whose slot is not a slot of the pool is not stored and
  *   raises HLWQ_DEVERR_KV_RANGE, as do requests whose rows are not in [0, T).
  * hlwq_kv_paged_attention: out = softmax(scale * q . k) v for every new token
- *   over the tokens up to itself, after the append of the same step; query
+ *   over the tokens up to itself, after the append of the same step (earlier
+ *   tokens of a chunk longer than R are seen as they were encoded); query
  *   heads g kv_heads-major (q_heads = kv_heads * group, head h * group + g
- *   reads kv head h).  fp32 softmax and sums, binary16 operands in the rotated
- *   domain, out rounded to bf16 once.  Keys in pages that are not in
+ *   reads kv head h).  fp32 softmax and sums; of the operands of the encoded
+ *   tokens' products the rotated query and the weights p times norm are
+ *   rounded to binary16 (relative 2^-11 at most), the centroids to about
+ *   2^-15; out is rounded to bf16 once.  Keys in pages that are not in
  *   [0, num_pages) are left out (HLWQ_DEVERR_KV_RANGE); a row that is left no
  *   key is 0.  A norm or a window value that is not finite concerns only the
  *   rows that see its token; such a row may be NaN throughout.  A request may
  *   have at most max_new tokens in the step; more raise HLWQ_DEVERR_KV_RANGE
  *   and the rows past the limit may stay unwritten.  out may be Q itself, with
  *   the same ld.
+ *   max_new also chooses the kernel for the whole call: one for few rows when
+ *   max_new * group <= 16, else tiles of 128 rows, in which a request with a
+ *   single token takes as long as one with 128 / group of them.  Requests b0 ..
+ *   b1 - 1 of a step can have a call of their own, with cu_new, n_past and
+ *   B = b1 - b0 from b0 on, the block table and the windows from row b0 on.
  *   workspace  device, 16-byte aligned, ws_bytes >= hlwq_workspace_bytes(
  *              HLWQ_OP_KV_ATTENTION, T, max_new, B, q_heads, kv_heads); its
  *              contents need not survive between calls, and calls that may

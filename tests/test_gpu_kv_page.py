@@ -914,3 +914,17 @@ def test_attention_reports_rows_out_of_range(hl, cb8, cu, past, max_new):
         args = (args[0], args[1], args[2], args[3][:1], *args[4:])
     hl.kv_paged_attention(args[0], _ints(cu), _ints(past), *args[3:-1], max(3, max_new), **kw)
     assert hl.device_error() == hl.DEVERR_KV_RANGE
+
+
+def test_attention_of_parts_of_a_step(hl, cb8):
+    """The decoding requests of a step and the one with a chunk in calls of their own, each
+    with the kernel for its lengths: together what one call gives."""
+    past, new = [100, 0, 37, 60, 300], [1, 1, 1, 50, 1]
+    args, kw, want, tol = _attend(hl, cb8, past, new, 2, 4, 16, 32, seed=17)
+    out = kw["out"]
+    Q, cu, n_past, table, kp, vp, (kw_, vw), cb, _ = args
+    for b0, b1, max_new in ((0, 3, 1), (3, 4, 50), (4, 5, 1)):
+        hl.kv_paged_attention(Q, cu[b0:b1 + 1], n_past[b0:b1], table[b0:b1], kp, vp, (kw_[b0:b1], vw[b0:b1]), cb, max_new, out=out)
+    torch.cuda.synchronize()
+    _check(out, want, tol, sum(new))
+    assert hl.device_error() == 0
