@@ -241,6 +241,10 @@ __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
 
+// On top of it for the window's products, so that 256 of them with any finite keys
+// stay finite: Q below 2^-9 in magnitude.
+constexpr float kWinScale = 1.0f / 65536.0f;
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -573,8 +577,8 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + C::kQFrag + s * 256),
-                     "r"(__byte_perm(__float_as_uint(v[4 * s]), __float_as_uint(v[4 * s + 1]), 0x7632)),
-                     "r"(__byte_perm(__float_as_uint(v[4 * s + 2]), __float_as_uint(v[4 * s + 3]), 0x7632))
+                     "r"(__byte_perm(__float_as_uint(v[4 * s] * kWinScale), __float_as_uint(v[4 * s + 1] * kWinScale), 0x7632)),
+                     "r"(__byte_perm(__float_as_uint(v[4 * s + 2] * kWinScale), __float_as_uint(v[4 * s + 3] * kWinScale), 0x7632))
                      : "memory");
       kv_fwht(v, lane);
       if (l8 == 0) qmul[r] = inv * a.scale * (kLog2e / 256.0f);
@@ -838,7 +842,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) qm[nt][k] = 256.0f * qmul[8 * nt + 2 * t4 + k];
+        for (int k = 0; k < 2; ++k) qm[nt][k] = 256.0f / kWinScale * qmul[8 * nt + 2 * t4 + k];
     }
 #pragma unroll 1
     for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {

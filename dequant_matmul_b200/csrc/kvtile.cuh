@@ -590,14 +590,14 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&y);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 z = __hmul2(p[k], sc);
+              const __nv_bfloat162 z = __hmul2(__hmul2(p[k], sc), __float2bfloat162_rn(kWinScale));
               x[4 * i + k] = *reinterpret_cast<const uint32_t*>(&z);
             }
           }
           tc_st16(row + kColQ + 16 * c, x);
         }
         tc_wait_st();
-        qm = sgn == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * q_inv * kLog2e, kMinQm);
+        qm = sgn == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * q_inv * (kLog2e / kWinScale), kMinQm);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);

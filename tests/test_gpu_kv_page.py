@@ -928,3 +928,16 @@ def test_attention_of_parts_of_a_step(hl, cb8):
     torch.cuda.synchronize()
     _check(out, want, tol, sum(new))
     assert hl.device_error() == 0
+
+
+@pytest.mark.parametrize("e", [-90, 60, 110, 121])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_window_key_magnitudes(hl, cb8, new, G, e):
+    """Exact keys 2^e times as large under a scale 2^-e times as large (all tokens in the window)."""
+    N, R = 60 + new, 128
+    X, Y, Q = _rows(N, 1, 83, False), _rows(N, 1, 84, False), _rows(new, G, 85, False)
+    args, kw, want, tol = _attend_on(hl, cb8, X, Y, Q, new, R, G)
+    window = ((args[6][0].double() * 2.0 ** e).to(torch.bfloat16), args[6][1])
+    out = hl.kv_paged_attention(*args[:6], window, *args[7:], scale=2.0 ** (-4 - e), **kw)
+    torch.cuda.synchronize()
+    _check(out, want, tol, new)
