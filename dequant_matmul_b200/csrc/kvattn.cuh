@@ -244,6 +244,9 @@ __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
 // On top of it for the window's products, so that 256 of them with any finite keys
 // stay finite: Q below 2^-9 in magnitude.
 constexpr float kWinScale = 1.0f / 65536.0f;
+// And the size that window values count with in their row's reference: p stays below
+// 2^-24, so that the sum of up to 2^20 finite values is finite.
+constexpr float kWinSize = 32.0f;
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -572,20 +575,21 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
       const float sc = pow2_scale(oct_max(mx), inv);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] *= sc;
+      for (int e = 0; e < 32; ++e) v[e] *= sc * kWinScale;
       // not rotated (for the window's keys): its bf16 bits, another exponent
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + C::kQFrag + s * 256),
-                     "r"(__byte_perm(__float_as_uint(v[4 * s] * kWinScale), __float_as_uint(v[4 * s + 1] * kWinScale), 0x7632)),
-                     "r"(__byte_perm(__float_as_uint(v[4 * s + 2] * kWinScale), __float_as_uint(v[4 * s + 3] * kWinScale), 0x7632))
+                     "r"(__byte_perm(__float_as_uint(v[4 * s]), __float_as_uint(v[4 * s + 1]), 0x7632)),
+                     "r"(__byte_perm(__float_as_uint(v[4 * s + 2]), __float_as_uint(v[4 * s + 3]), 0x7632))
                      : "memory");
       kv_fwht(v, lane);
       if (l8 == 0) qmul[r] = inv * a.scale * (kLog2e / 256.0f);
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + s * 256),
-                     "r"(pack_half2(v[4 * s], v[4 * s + 1])), "r"(pack_half2(v[4 * s + 2], v[4 * s + 3]))
+                     "r"(pack_half2(v[4 * s] / kWinScale, v[4 * s + 1] / kWinScale)),
+                     "r"(pack_half2(v[4 * s + 2] / kWinScale, v[4 * s + 3] / kWinScale))
                      : "memory");
     }
     __syncthreads();
@@ -811,11 +815,14 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 
     // ---- out of the rotated domain: O^T <- H O^T / (256 kNvScale), in registers
     if (ta < e_tb) {
-      const float f = back / (256.0f * kNvScale);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+          const float nm = m[nt][k] + kWinSize, c = ex2(m[nt][k] - nm);  // the window's reference, at once
+          const float f = c * back / (256.0f * kNvScale);
+          l[nt][k] *= c;
+          m[nt][k] = nm;
           float v[32];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[2 * i] = o[nt][i][k] * f, v[2 * i + 1] = o[nt][i][2 + k] * f;
@@ -869,9 +876,9 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
         }
       }
-      const float one[1][2] = {{1.0f, 1.0f}}, zero[1][2] = {{0.0f, 0.0f}};
+      const float one[1][2] = {{1.0f, 1.0f}}, size[1][2] = {{kWinSize, kWinSize}};
       const int key[1] = {k0 + g}, end[1] = {w_end};
-      score(d, one, zero, key, end);
+      score(d, one, size, key, end);
       uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)

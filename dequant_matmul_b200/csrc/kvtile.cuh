@@ -424,6 +424,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           my = fmaxf(fmaxf(y.x, y.y), my);
         }
         mx = __fmul_ru(fmaxf(mx, my), qm);
+        if constexpr (kWin) mx = __fadd_ru(mx, kWinSize);
         // also: both halves of S have been read, P may take its place
         if (pair_any(quarter, !got || mx > __fadd_rd(m, 8.0f))) {  // seldom
           if (pair_any(quarter, !got)) return false;
@@ -550,7 +551,10 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         // O out of the rotated domain
         within_blocks(row, half);
         pair_sync(quarter);
-        const float f = back / (256.0f * kNvScale);
+        const float nm = m + kWinSize, corr = ex2(m - nm);  // the window's reference, at once
+        const float f = corr * back / (256.0f * kNvScale);
+        l *= corr;
+        m = nm;
         across_blocks(row, half, [&](int c, const float(&v)[64]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

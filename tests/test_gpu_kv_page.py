@@ -941,3 +941,20 @@ def test_attention_window_key_magnitudes(hl, cb8, new, G, e):
     out = hl.kv_paged_attention(*args[:6], window, *args[7:], scale=2.0 ** (-4 - e), **kw)
     torch.cuda.synchronize()
     _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("e", [-100, 60, 110, 122])
+@pytest.mark.parametrize("flat", [False, True])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_window_value_magnitudes(hl, cb8, new, G, flat, e):
+    """Exact values 2^e times as large give outputs 2^e times as large; with flat weights
+    and one sign their plain sum would overflow."""
+    N, R = 90 + new, 160
+    X, Y, Q = _rows(N, 1, 86, False), _rows(N, 1, 87, False), _rows(new, G, 88, False)
+    if flat:
+        Y, Q = Y.abs(), (Q.double() * 2.0 ** -20).to(torch.bfloat16)
+    args, kw, want, tol = _attend_on(hl, cb8, X, Y, Q, new, R, G)
+    window = (args[6][0], (args[6][1].double() * 2.0 ** e).to(torch.bfloat16))
+    out = hl.kv_paged_attention(*args[:6], window, *args[7:], **kw)
+    torch.cuda.synchronize()
+    _check(out.double() * 2.0 ** -e, want, tol, new)
