@@ -101,19 +101,35 @@ __device__ __forceinline__ KvItem kv_item(const KvAttn& a, int pair, int tiles, 
   return it;
 }
 
+// The pair to look at after `pair`: a request without rows left in it has none further
+// on, so at most one of them is looked at (a request may have far fewer rows than
+// max_new's tiles, which only bound them).
+__device__ __forceinline__ int kv_after(const KvItem& it, int pair, int tiles) {
+  return it.cost ? pair + 1 : (it.b + 1) * tiles;
+}
+
+// The pairs [first, last) of this thread of kThreads.
+template <int kThreads>
+__device__ __forceinline__ void kv_mine(const KvAttn& a, int tiles, int& first, int& last) {
+  const int64_t pairs = static_cast<int64_t>(a.B) * tiles, per = (pairs + kThreads - 1) / kThreads;
+  first = static_cast<int>(min(threadIdx.x * per, pairs));
+  last = static_cast<int>(min(first + per, pairs));
+}
+
 // The total of all costs; `mine0` = the cost before this thread's pairs.  Called
 // by all kThreads threads of the CTA.
 template <int kRows, int kWinUnit, int kItemCost, int kThreads>
 __device__ __forceinline__ int64_t kv_total_cost(const KvAttn& a, int tiles, int64_t* warp_sums, int64_t& mine0) {
-  const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int pair, last;
+  kv_mine<kThreads>(a, tiles, pair, last);
   int64_t sum = 0;
   bool bad = false;
 #pragma unroll 1
-  for (int i = 0; i < per; ++i) {
-    const int pair = threadIdx.x * per + i;
-    if (pair >= pairs) break;
-    sum += kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad).cost;
+  while (pair < last) {
+    const KvItem it = kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad);
+    sum += it.cost;
+    pair = kv_after(it, pair, tiles);
   }
   if (bad) raise_device_error(HLWQ_DEVERR_KV_RANGE);
   int64_t inc = sum;
@@ -138,21 +154,21 @@ __device__ __forceinline__ int64_t kv_total_cost(const KvAttn& a, int tiles, int
 // pairs contain it and published in found[0] (pair) and found[1] (where its cost begins).
 template <int kRows, int kWinUnit, int kItemCost, int kThreads>
 __device__ __forceinline__ void kv_find(const KvAttn& a, int tiles, int64_t mine0, int64_t want, int64_t* found) {
-  const int pairs = a.B * tiles, per = (pairs + kThreads - 1) / kThreads;
+  int pair, last;
+  kv_mine<kThreads>(a, tiles, pair, last);
   int64_t u = mine0;
   bool bad = false;
   if (u <= want) {
 #pragma unroll 1
-    for (int i = 0; i < per; ++i) {
-      const int pair = threadIdx.x * per + i;
-      if (pair >= pairs) break;
-      const int64_t n = kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad).cost;
-      if (want < u + n) {
+    while (pair < last) {
+      const KvItem it = kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad);
+      if (want < u + it.cost) {
         found[0] = pair;
         found[1] = u;
         break;
       }
-      u += n;
+      u += it.cost;
+      pair = kv_after(it, pair, tiles);
     }
   }
   __syncthreads();
@@ -202,7 +218,8 @@ struct KvWalk {
     while (u < u1) {
       while (u >= at + it.cost) {
         at += it.cost;
-        it = kv_item<kRows, kWinUnit, kItemCost>(a, ++pair, tiles, bad);
+        pair = kv_after(it, pair, tiles);
+        it = kv_item<kRows, kWinUnit, kItemCost>(a, pair, tiles, bad);
       }
       const int each = it.units + kItemCost;
       h = static_cast<int>((u - at) / each);

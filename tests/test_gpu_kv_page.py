@@ -958,3 +958,34 @@ def test_attention_window_value_magnitudes(hl, cb8, new, G, flat, e):
     out = hl.kv_paged_attention(*args[:6], window, *args[7:], **kw)
     torch.cuda.synchronize()
     _check(out.double() * 2.0 ** -e, want, tol, new)
+
+
+def test_attention_of_few_tokens_under_the_largest_max_new(hl, cb8):
+    """B times max_new's row tiles just below its limit of 2^31: two requests of thousands have
+    tokens, and the bound costs nothing that grows with it."""
+    B, T, G, R, P = 8191, 262176 * 2, 64, 4, 16
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("Q of 17 GB")
+    X, Y, q = _rows(50, 1, 90, False), _rows(50, 1, 91, False), _rows(3, G, 92, False)
+    args, kw, want, tol = _attend_on(hl, cb8, X, Y, q, 3, R, G)
+    past, new = torch.zeros(B, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+    past[[40, 8190]], new[[40, 8190]] = 47, 3
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32), new.cumsum(0).int()])
+    table = torch.full((B, args[3].shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[[40, 8190]] = args[3]
+    window = []
+    for w in args[6]:
+        window.append(torch.zeros(B, 1, R, 256, dtype=torch.bfloat16, device="cuda"))
+        window[-1][[40, 8190]] = w
+    Q = torch.empty(T, G, 256, dtype=torch.bfloat16, device="cuda")
+    Q[:6] = torch.cat([q, q]).cuda()
+    Q[6] = 7.0
+    call = (Q, cu.cuda(), past.cuda(), table, *args[4:6], tuple(window), cb8, T)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ends[0].record()
+    hl.kv_paged_attention(*call, out=Q)
+    ends[1].record()
+    torch.cuda.synchronize()
+    assert hl.device_error() == 0
+    _check(Q[:7].cpu(), np.concatenate([want, want]), np.concatenate([tol, tol]), 6)
+    assert ends[0].elapsed_time(ends[1]) < 100
