@@ -262,8 +262,17 @@ __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
 // stay finite: Q below 2^-9 in magnitude.
 constexpr float kWinScale = 1.0f / 65536.0f;
 // And the size that window values count with in their row's reference: p stays below
-// 2^-24, so that the sum of up to 2^20 finite values is finite.
+// 2^-24, so that the sum of up to 2^20 finite values is finite.  (p is above 2^-32 for the
+// row's largest score: values below 2^-94 are multiplied as fp32 subnormals.)
 constexpr float kWinSize = 32.0f;
+
+// A row's reference is one number m, score + log2 norm, while its magnitude is at most
+// kFar (steps of 2^-7).  Beyond it rounding the sum would take the row's largest weight
+// away (from 2^27 on p n is 0 in binary16): the row's scores then count from one of them,
+// its shift, and m is a small number again, at most kFarNext (beyond it the shift
+// follows) and the window's size.  A result that is joined with others has
+// shift + kFarEnd in one number, its weights brought to that.
+constexpr float kFar = 65536.0f, kFarNext = 64.0f, kFarEnd = kFarNext + kWinSize;
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -611,7 +620,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     }
     __syncthreads();
 
-    float o[NT][16][4], m[NT][2], l[NT][2], qm[NT][2];
+    float o[NT][16][4], m[NT][2], shift[NT][2], l[NT][2], qm[NT][2];
     int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -619,7 +628,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       for (int k = 0; k < 2; ++k) {
         const int r = 8 * nt + 2 * t4 + k;
         m[nt][k] = kMinM;
-        l[nt][k] = 0.0f;
+        shift[nt][k] = l[nt][k] = 0.0f;
         qm[nt][k] = qmul[r] * back;
         lim[nt][k] = r < nrows ? it.p + (it.row0 + r) / a.G + 1 : 0;
 #pragma unroll
@@ -629,48 +638,82 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     // scores of M tiles of 16 keys, times their factors f[.][0] (this lane's first
     // key, index key[.]) and f[.][1] (8 further), with the log2 of their values' size
     // in size[.][.]; keys from end[.] on are not there.  The rows' references follow;
-    // d becomes p = exp2(s - reference).  Rounded so that p size never passes 2^8
+    // d becomes p = exp2(s - shift - m)
     auto score = [&](auto& d, const auto& f, const auto& size, const auto& key, const auto& end) {
       constexpr int M = sizeof(key) / sizeof(key[0]);
+      // the largest score less shift + size, of two rows
+      auto largest = [&](int nt) -> float2 {
+        float2 x = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 t = add2(add2(make_float2(d[i][nt][2 * j], d[i][nt][2 * j + 1]), make_float2(-shift[nt][0], -shift[nt][1])),
+                                  make_float2(size[i][j], size[i][j]));
+            x.x = fmaxf(x.x, t.x);
+            x.y = fmaxf(x.y, t.y);
+          }
+        return x;
+      };
+      auto row_max = [](float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+      };
+      float2 x[NT];
       bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const bool none = m[nt][k] == kMinM;  // no key so far
-          const float ref = none ? 0.0f : m[nt][k];
-          float x = -INFINITY;
+        for (int i = 0; i < M; ++i)
 #pragma unroll
-          for (int i = 0; i < M; ++i) {
-            const int see = min(lim[nt][k], end[i]);
-            d[i][nt][k] = key[i] < see ? fmaf(d[i][nt][k], f[i][0] * qm[nt][k], -ref) : -INFINITY;
-            d[i][nt][2 + k] = key[i] + 8 < see ? fmaf(d[i][nt][2 + k], f[i][1] * qm[nt][k], -ref) : -INFINITY;
-            x = fmaxf(x, fmaxf(d[i][nt][k] + size[i][0], d[i][nt][2 + k] + size[i][1]));
+          for (int j = 0; j < 2; ++j) {
+            // rounded here: the selection keeps it from being fused with the shift's subtraction,
+            // where the score that a shift was taken from has to come out 0
+            const float2 s = mul2(make_float2(d[i][nt][2 * j], d[i][nt][2 * j + 1]),
+                                  mul2(make_float2(f[i][j], f[i][j]), make_float2(qm[nt][0], qm[nt][1])));
+            d[i][nt][2 * j] = key[i] + 8 * j < min(lim[nt][0], end[i]) ? s.x : -INFINITY;
+            d[i][nt][2 * j + 1] = key[i] + 8 * j < min(lim[nt][1], end[i]) ? s.y : -INFINITY;
           }
-          over |= x > (none ? kMinM : 8.0f);
-        }
+        x[nt] = largest(nt);
+        over |= x[nt].x > m[nt][0] + 8.0f || x[nt].y > m[nt][1] + 8.0f;
+      }
       if (__any_sync(0xffffffffu, over)) {
+        float nm[NT][2];
+        bool big = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float ref = m[nt][k] == kMinM ? 0.0f : m[nt][k];
-            float x = -INFINITY;
+            nm[nt][k] = fmaxf(m[nt][k], row_max(k ? x[nt].y : x[nt].x));
+            big |= nm[nt][k] > m[nt][k] && fabsf(nm[nt][k]) > (shift[nt][k] == 0.0f ? kFar : kFarNext);
+          }
+        if (__any_sync(0xffffffffu, big)) {
 #pragma unroll
-            for (int i = 0; i < M; ++i)
-              x = fmaxf(x, fmaxf(__fadd_ru(d[i][nt][k], size[i][0]), __fadd_ru(d[i][nt][2 + k], size[i][1])));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float nm = fmaxf(m[nt][k], __fadd_ru(ref, x)), c = ex2(m[nt][k] - nm);
-            const float step = nm == kMinM ? 0.0f : __fadd_rd(ref, -nm);
-            m[nt][k] = nm;
-            l[nt][k] *= c;
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < M; ++i) {
-              d[i][nt][k] += step;
-              d[i][nt][2 + k] += step;
+            for (int k = 0; k < 2; ++k) {
+              float s = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < M; ++i) s = fmaxf(s, fmaxf(d[i][nt][k], d[i][nt][2 + k]));
+              s = row_max(s);
+              if (nm[nt][k] > m[nt][k] && fabsf(nm[nt][k]) > (shift[nt][k] == 0.0f ? kFar : kFarNext)) {
+                if (m[nt][k] != kMinM) m[nt][k] += __fsub_rn(shift[nt][k], s);
+                shift[nt][k] = s;
+              }
             }
+            const float2 y = largest(nt);
+            nm[nt][0] = fmaxf(m[nt][0], row_max(y.x));
+            nm[nt][1] = fmaxf(m[nt][1], row_max(y.y));
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float c = ex2(m[nt][k] - nm[nt][k]);
+            m[nt][k] = nm[nt][k];
+            l[nt][k] *= c;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               o[nt][i][k] *= c;
@@ -679,14 +722,21 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float2 sum = make_float2(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
+        for (int i = 0; i < M; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) d[i][nt][k] = ex2(d[i][nt][k]);
-          l[nt][0] += d[i][nt][0] + d[i][nt][2];
-          l[nt][1] += d[i][nt][1] + d[i][nt][3];
-        }
+          for (int j = 0; j < 2; ++j) {
+            const float2 t = add2(add2(make_float2(d[i][nt][2 * j], d[i][nt][2 * j + 1]), make_float2(-shift[nt][0], -shift[nt][1])),
+                                  make_float2(-m[nt][0], -m[nt][1]));
+            d[i][nt][2 * j] = ex2(t.x);
+            d[i][nt][2 * j + 1] = ex2(t.y);
+            sum = add2(sum, make_float2(d[i][nt][2 * j], d[i][nt][2 * j + 1]));
+          }
+        l[nt][0] = sum.x;
+        l[nt][1] = sum.y;
+      }
     };
 
     // ---- encoded keys: each warp a contiguous part of the segment's tiles of 16,
@@ -955,6 +1005,20 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
     }
 
     // ---- the four warps' results: common maximum, sums, and O
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (shift[nt][k] != 0.0f) {
+          const float c = ex2(m[nt][k] - kFarEnd);
+          m[nt][k] = shift[nt][k] + kFarEnd;
+          l[nt][k] *= c;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            o[nt][i][k] *= c;
+            o[nt][i][2 + k] *= c;
+          }
+        }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

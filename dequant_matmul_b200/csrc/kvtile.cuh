@@ -72,6 +72,7 @@ constexpr int kKvTile = 64 * 256 * 2;                // one K or V^T tile
 constexpr int kNrmSlot = 192 * 4 + 16;               // K norms, V norms (kNvScale times), log2_above of V's, mask
 constexpr int kSlotMask = 192 * 4;
 constexpr float kMinQm = 1e-36f;                     // encoded scores of less are 0; log2_above / kMinQm is finite
+constexpr int kPasses = 3;                           // of a tile while rows' shifts move: the third finds them exact
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 constexpr int kAtSmem = 8192 /*align*/ + 8192 /*table*/ + 4 * kKvTile + kCodeStages * kCodeStage + 4 * kNrmSlot + 512 +
                         2 * kAtRows * 4 /*row exchange*/;
@@ -366,6 +367,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       // m: the row's reference, which follows its largest p n as in the few-row
       // kernel; l: this thread's share of the row's sum
       float m = kMinM, l = 0.0f, qm = 0.0f, inv_qm = 0.0f;
+      float shift = 0.0f;    // what is taken off the row's scores first, where they are large
+      bool far = false;      // any row of the two warps has one
       float q_inv = 0.0f;    // what takes the row's power of two back (0: not looked for yet)
       bool started = false;  // O holds something
 
@@ -378,7 +381,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         const bool got = at_wait_warp(s_full + 8 * s, par);
         tc_fence_after();
         float2 v[8][2];
-        {
+        for (int pass = 0;; ++pass) {  // again where a row's shift moves
           uint32_t x[8][4];
 #pragma unroll
           for (int i = 0; i < 8; ++i) tc_ld4(sc + 8 * i + 4 * half, x[i]);
@@ -388,52 +391,73 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             v[i][0] = make_float2(__uint_as_float(x[i][0]), __uint_as_float(x[i][1]));
             v[i][1] = make_float2(__uint_as_float(x[i][2]), __uint_as_float(x[i][3]));
           }
-        }
-        if constexpr (!kWin) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 x = lds_f4(nb + 32 * i);
-            v[i][0] = mul2(v[i][0], make_float2(x.x, x.y));
-            v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
-          }
-        }
-        const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + kSlotMask);  // 16-key groups whose page is there
-        const int see = min(lim, end) - k0;
-        if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
-          const int sh = see - 2 * half;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int f = at_key(8 * i);
-            if (f >= sh || !(there & 1u)) v[i][0].x = -INFINITY;
-            if (f + 16 >= sh || !(there & 2u)) v[i][0].y = -INFINITY;
-            if (f + 32 >= sh || !(there & 4u)) v[i][1].x = -INFINITY;
-            if (f + 48 >= sh || !(there & 8u)) v[i][1].y = -INFINITY;
-          }
-        }
-        // the largest score + log2 norm, rounded so that p n never passes 2^8
-        float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float2 x = v[i][0], y = v[i][1];
           if constexpr (!kWin) {
-            const float4 z = lds_f4(nb + 512 + 32 * i);
-            x = fma2_up(make_float2(z.x, z.y), make_float2(inv_qm, inv_qm), x);
-            y = fma2_up(make_float2(z.z, z.w), make_float2(inv_qm, inv_qm), y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 x = lds_f4(nb + 32 * i);
+              v[i][0] = mul2(v[i][0], make_float2(x.x, x.y));
+              v[i][1] = mul2(v[i][1], make_float2(x.z, x.w));
+            }
           }
-          mx = fmaxf(fmaxf(x.x, x.y), mx);
-          my = fmaxf(fmaxf(y.x, y.y), my);
-        }
-        mx = __fmul_ru(fmaxf(mx, my), qm);
-        if constexpr (kWin) mx = __fadd_ru(mx, kWinSize);
-        // also: both halves of S have been read, P may take its place
-        if (pair_any(quarter, !got || mx > __fadd_rd(m, 8.0f))) {  // seldom
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) v[i][k] = make_float2(__fsub_rn(v[i][k].x, shift), __fsub_rn(v[i][k].y, shift));
+          }
+          const uint32_t there = kWin ? 15u : lds32(nb - 16 * half + kSlotMask);  // 16-key groups whose page is there
+          const int see = min(lim, end) - k0;
+          if (__any_sync(0xffffffffu, see < 64) || there != 15u) {
+            const int sh = see - 2 * half;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int f = at_key(8 * i);
+              if (f >= sh || !(there & 1u)) v[i][0].x = -INFINITY;
+              if (f + 16 >= sh || !(there & 2u)) v[i][0].y = -INFINITY;
+              if (f + 32 >= sh || !(there & 4u)) v[i][1].x = -INFINITY;
+              if (f + 48 >= sh || !(there & 8u)) v[i][1].y = -INFINITY;
+            }
+          }
+          // the largest score + log2 norm, rounded so that p n never passes 2^8
+          float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 x = v[i][0], y = v[i][1];
+            if constexpr (!kWin) {
+              const float4 z = lds_f4(nb + 512 + 32 * i);
+              x = fma2_up(make_float2(z.x, z.y), make_float2(inv_qm, inv_qm), x);
+              y = fma2_up(make_float2(z.z, z.w), make_float2(inv_qm, inv_qm), y);
+            }
+            mx = fmaxf(fmaxf(x.x, x.y), mx);
+            my = fmaxf(fmaxf(y.x, y.y), my);
+          }
+          mx = __fmul_ru(fmaxf(mx, my), qm);
+          if constexpr (kWin) mx = __fadd_ru(mx, kWinSize);
+          // also: both halves of S have been read, P may take its place
+          if (!pair_any(quarter, !got || mx > __fadd_rd(m, 8.0f))) break;  // nearly always
           if (pair_any(quarter, !got)) return false;
           *mine = mx;
           pair_sync(quarter);
           const float nm = fmaxf(m, fmaxf(mx, *other));
+          pair_sync(quarter);
+          const bool big = nm > m && fabsf(nm) > (far ? kFarNext : kFar);
+          if (pass < kPasses && __any_sync(0xffffffffu, big)) {  // the other warp has the same rows
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fmaxf(v[i][0].x, v[i][0].y), fmaxf(v[i][1].x, v[i][1].y)));
+            *mine = top;
+            pair_sync(quarter);
+            if (big) {
+              const float to = shift + fmaxf(top, *other);
+              if (m != kMinM) m = fmaf(shift - to, qm, m);
+              shift = to;
+            }
+            far = true;
+            pair_sync(quarter);
+            continue;
+          }
           const float corr = ex2(m - nm);
           m = nm;
-          pair_sync(quarter);
           l *= corr;
           if (started) {  // rescale O once the product before has been added
             if (pair_any(quarter, !pv_done(gt - 1))) return false;
@@ -447,6 +471,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
               tc_st16(row + kColO + c, x);
             }
           }
+          break;
         }
         // p = 2^(s qm - m), and its sum
         const float2 q2 = make_float2(qm, qm), b2 = make_float2(-m, -m);
@@ -601,7 +626,9 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
           tc_st16(row + kColQ + 16 * c, x);
         }
         tc_wait_st();
+        const float was = qm;
         qm = sgn == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * q_inv * (kLog2e / kWinScale), kMinQm);
+        if (far) shift *= was / qm;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
@@ -617,6 +644,12 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
       l = half ? *other + l : l + *other;
       const bool whole = w.ta == 0 && w.tb == it.units;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float fold = 1.0f;
+      if (far && shift != 0.0f) {  // one number for the reference again, the rest of it in the part
+        fold = ex2(m - kFarEnd);
+        l *= fold;
+        m = fmaf(shift, qm, kFarEnd);
+      }
       uint16_t* orow = a.out + static_cast<int64_t>(it.c0 + tok) * a.ldo + head * kKvDim;
       float* part = parts + static_cast<int64_t>(2 * blockIdx.x + (w.ta == 0 ? 1 : 0)) * (kAtRows * (kKvDim + 2));
 #pragma unroll 1
@@ -634,6 +667,8 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
             reinterpret_cast<uint4*>(orow + c)[k] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else if (on) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fold);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // [256 columns / 4][row][4]: a warp writes 512 bytes at a time
             reinterpret_cast<uint4*>(part)[(c / 4 + k) * kAtRows + r] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);

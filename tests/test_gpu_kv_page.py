@@ -989,3 +989,46 @@ def test_attention_of_few_tokens_under_the_largest_max_new(hl, cb8):
     assert hl.device_error() == 0
     _check(Q[:7].cpu(), np.concatenate([want, want]), np.concatenate([tol, tol]), 6)
     assert ends[0].elapsed_time(ends[1]) < 100
+
+
+@pytest.mark.parametrize("e", [16, 24, 30, 100])
+@pytest.mark.parametrize("R", [0, 60, 400])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_scores_of_any_size(hl, cb8, new, G, R, e):
+    """One key's score is far above the others' (all of them below 0 or not), at sizes of
+    2^18 to 2^106, where neighbouring fp32 numbers are up to 2^82 apart: its value is the
+    output, with the tolerance of a single term."""
+    N = 160 + new
+    for hot in (3, N - new - 1):
+        for sign in (1, -1):
+            X, Y, Q, base = _small_values(N, new, G, 95)
+            if sign < 0:
+                X = ((0.1 * X.float() - base) * (1 + torch.arange(N)[:, None, None] / N)).to(torch.bfloat16)
+            X[hot, 0] = ((3 if sign > 0 else -0.25) * base).to(torch.bfloat16)
+            Y[80, 0] = 3750.0 * torch.sign(Y[80, 0].float()).to(torch.bfloat16)
+            args, kw, want, tol = _attend_on(hl, cb8, X, Y, (Q.double() * 2.0 ** e).to(torch.bfloat16), new, R, G)
+            assert np.ptp(want.reshape(-1, 256), axis=0).max() == 0 and tol.max() < 0.02 * np.linalg.norm(want[0, 0])
+            out = hl.kv_paged_attention(*args, **kw)
+            torch.cuda.synchronize()
+            _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("e", [16, 24, 60])
+@pytest.mark.parametrize("R", [0, 400])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_equal_keys_at_scores_of_any_size(hl, cb8, new, G, R, e):
+    """Two keys that are the same and far above the others have half the weight each,
+    whichever tiles and parts they are in: equal scores are rounded alike."""
+    N = 200 + new
+    for pair in ((3, 5), (3, 70), (20, N - new - 1)):
+        X, Y, Q, base = _small_values(N, new, G, 99)
+        X[list(pair), 0] = (3 * base).to(torch.bfloat16)
+        args, kw, want, _ = _attend_on(hl, cb8, X, Y, (Q.double() * 2.0 ** e).to(torch.bfloat16), new, R, G)
+        # half a bf16 step of the output; p n rounded (2^-11) and centroids (2^-13) of two terms
+        # no larger than twice the output's norm together
+        tol = (2.0 ** -8 + 2 * (2.0 ** -11 + 2.0 ** -13)) * np.linalg.norm(want, axis=-1)
+        sizes = [np.linalg.norm(Y[i, 0].double().numpy()) for i in pair]
+        assert sum(sizes) / 2 < 2 * np.linalg.norm(want[0, 0])
+        out = hl.kv_paged_attention(*args, **kw)
+        torch.cuda.synchronize()
+        _check(out, want, tol, new)
