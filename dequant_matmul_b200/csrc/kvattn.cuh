@@ -261,6 +261,11 @@ __device__ __forceinline__ float pow2_scale(float mx, float& inv) {
 // On top of it for the window's products, so that 256 of them with any finite keys
 // stay finite: Q below 2^-9 in magnitude.
 constexpr float kWinScale = 1.0f / 65536.0f;
+// The factor that takes it back, with the query's own, passes fp32 for the largest
+// queries.  It stops at the largest finite number: their scores are beyond 2^100 and stay
+// as far apart as weights tell.
+constexpr float kMaxFinite = 3.402823466e38f;
+__device__ __forceinline__ float window_qm(float x) { return fminf(fmaxf(x, -kMaxFinite), kMaxFinite); }
 // And the size that window values count with in their row's reference: p stays below
 // 2^-24, so that the sum of up to 2^20 finite values is finite.  (p is above 2^-32 for the
 // row's largest score: values below 2^-94 are multiplied as fp32 subnormals.)
@@ -498,7 +503,7 @@ constexpr int kStages = 4;
 constexpr int kRowItemCost = 5;
 constexpr int kRowWinUnit = 16;
 constexpr int kTabBytes = 64 * 128;
-constexpr float kMinM = -3.402823466e38f;
+constexpr float kMinM = -kMaxFinite;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNvScale = 128.0f;  // on the norms of values: p n kNvScale < 2^15
 
@@ -916,7 +921,7 @@ kv_attn_rows_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) qm[nt][k] = 256.0f / kWinScale * qmul[8 * nt + 2 * t4 + k];
+        for (int k = 0; k < 2; ++k) qm[nt][k] = window_qm(256.0f / kWinScale * qmul[8 * nt + 2 * t4 + k]);
     }
 #pragma unroll 1
     for (int k0 = w_first + 16 * warp; k0 < w_end; k0 += 16 * kRowWarps) {

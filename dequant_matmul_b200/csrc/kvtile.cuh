@@ -627,7 +627,7 @@ kv_attn_tile_kernel(const KvAttn a, int tiles, float* __restrict__ parts, KvCut*
         }
         tc_wait_st();
         const float was = qm;
-        qm = sgn == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * q_inv * (kLog2e / kWinScale), kMinQm);
+        qm = sgn == 0.0f ? 1.0f : fmaxf(window_qm(fabsf(a.scale) * q_inv * (kLog2e / kWinScale)), kMinQm);
         if (far) shift *= was / qm;
         tc_fence_before();
         __syncwarp();

@@ -1032,3 +1032,19 @@ def test_attention_equal_keys_at_scores_of_any_size(hl, cb8, new, G, R, e):
         out = hl.kv_paged_attention(*args, **kw)
         torch.cuda.synchronize()
         _check(out, want, tol, new)
+
+
+@pytest.mark.parametrize("e", [118, 122, 124])
+@pytest.mark.parametrize("new,G", ROWS)
+def test_attention_largest_queries_with_a_window(hl, cb8, new, G, e):
+    """Queries near the top of bf16's range whose scores fp32 holds: the key with the
+    largest score wins, and no row comes out NaN."""
+    N, R = 60 + new, 128
+    X, Y, Q, base = _small_values(N, new, G, 97)
+    X[5, 0] = 3 * base
+    X = (X.float() * 2.0 ** -6).to(torch.bfloat16)
+    args, kw, want, tol = _attend_on(hl, cb8, X, Y, (Q.double() * 2.0 ** e).to(torch.bfloat16), new, R, G)
+    assert np.ptp(want.reshape(-1, 256), axis=0).max() == 0 and tol.max() < 0.02 * np.linalg.norm(want[0, 0])
+    out = hl.kv_paged_attention(*args, **kw)
+    torch.cuda.synchronize()
+    _check(out, want, tol, new)
