@@ -486,12 +486,12 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 //
 // Bound: HBM by its bytes (196 per token and kv head); in fact integer instructions
 // and shared-memory reads, one warp instruction in five a table read.  64 requests
-// of 64 to 16384 tokens, 4 kv heads of 6 rows (438 MB): 163 us, 2.7 TB/s, DRAM
+// of 64 to 16384 tokens, 4 kv heads of 6 rows (438 MB): 167 us, 2.6 TB/s, DRAM
 // traffic equal to the bytes, 730 warp instructions per 16 keys at 2.3 per cycle
-// (ALU pipe 59 %, shared memory 57 %).  A tcgen05 kernel would have to write the decoded
+// (ALU pipe 58 %, shared memory 56 %).  A tcgen05 kernel would have to write the decoded
 // tiles to shared memory first, as much traffic again as the table reads; the
 // legacy instruction takes them from registers, and with 8 or 16 rows its
-// rate is no limit (tensor pipe 21 %).
+// rate is no limit (tensor pipe 20 %).
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;

@@ -963,9 +963,9 @@ int launch_tiles(const KvAttn& a, int ctas, int tiles, float* parts, KvCut* cuts
 // few-row kernel up to 16 rows per kv head, the tensor-core tiles above.  Measured, us
 // for 16 requests of 100 to 7000 tokens and 8 kv heads / one of 60000 tokens and 4:
 //   rows              8           12           16           18           24           32           48
-//   tiles of 8     75 / 50    103 / 60     103 / 60     137 / 73     143 / 75     169 / 89     298 / 118
-//   tiles of 16    91 / 58     91 / 60      91 / 60     145 / 71     146 / 73     149 / 73     239 / 103
-//   tiles of 128  132 / 89    124 / 97     126 / 93     128 / 97     126 / 93     124 / 91     157 / 93
+//   tiles of 8     58 / 42     95 / 52      94 / 53     125 / 67     126 / 67     154 / 82     218 / 111
+//   tiles of 16    78 / 51     81 / 51      83 / 53     153 / 68     154 / 69     158 / 69     208 / 97
+//   tiles of 128  106 / 79    108 / 80     108 / 81     109 / 81     109 / 81     109 / 81     111 / 81
 // (One request alone would do better on two tiles of 16 up to 32 rows; batches would not.)
 struct KvGrid {
   int rows, ctas;
